@@ -27,7 +27,7 @@ FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, "fp4q.hip")]
+    return [os.path.join(CSRC, f) for f in ("fp4q.hip", "attention.hip")]
 
 
 def deps():
@@ -38,11 +38,27 @@ def deps():
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    objs = ["%s.%s.o" % (tmp, os.path.basename(src)) for src in sources()]
+    cflags = [f for f in FLAGS if f != "-shared"]
+    jobs = [[HIPCC, *cflags, "-c", src, "-o", obj] for src, obj in zip(sources(), objs)]
+    link = [HIPCC, *FLAGS, *objs, "-o", tmp]
+    try:
+        running = []
+        for cmd in jobs:                 # the sources compile side by side
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append(subprocess.Popen(cmd))
+        failed = [cmd for cmd, p in zip(jobs, running) if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
+        if verbose:
+            print(" ".join(link), flush=True)
+        subprocess.check_call(link)
+        os.replace(tmp, LIB)
+    finally:
+        for f in objs:
+            if os.path.exists(f):
+                os.remove(f)
     return LIB
 
 
@@ -56,9 +72,11 @@ def up_to_date() -> bool:
 def dump_asm(out_dir: str) -> str:
     """Device assembly of the kernels, for inspection."""
     os.makedirs(out_dir, exist_ok=True)
-    cmd = [HIPCC, *[f for f in FLAGS if f not in ("-shared", "-fPIC")],
-           "--cuda-device-only", "-S", *sources(), "-o", os.path.join(out_dir, "fp4q-gfx950.s")]
-    subprocess.check_call(cmd)
+    for src in sources():
+        name = os.path.splitext(os.path.basename(src))[0]
+        cmd = [HIPCC, *[f for f in FLAGS if f not in ("-shared", "-fPIC")],
+               "--cuda-device-only", "-S", src, "-o", os.path.join(out_dir, name + "-gfx950.s")]
+        subprocess.check_call(cmd)
     return os.path.join(out_dir, "fp4q-gfx950.s")
 
 

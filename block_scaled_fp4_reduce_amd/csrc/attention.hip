@@ -1,0 +1,236 @@
+// attention.hip -- entry points of the norm with rotation and of attention
+// over the paged FP4 cache: argument checks on the host, then kernel
+// launches on the caller's stream.  See include/fp4q.h for the contract.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "host_common.h"
+#include "kv_attention_kernels.h"
+#include "kv_host.h"
+#include "rope_kernels.h"
+
+using namespace fp4q;
+
+namespace {
+
+// ------------------------------------------------------------------ norm + rotation
+// Lanes per head: D / 8 rounded up to a power of two.
+int lanes_per_head(int dim) {
+  int l = 1;
+  while (l * 8 < dim) l *= 2;
+  return l;
+}
+
+int check_tokens(int64_t tokens, int64_t stride, int64_t width) {
+  if (stride < width || stride % 8 || stride >= kMaxElems) return FP4_E_SHAPE;
+  if (tokens > 0 && stride > kMaxElems / tokens) return FP4_E_SHAPE;
+  return FP4_OK;
+}
+
+int check_rope(const fp4_qk_rope* a) {
+  if (!a) return FP4_E_NULL;
+  if (a->tokens < 0 || a->tokens >= ((int64_t)1 << 31) || a->q_heads < 0 || a->k_heads < 0 ||
+      a->q_heads > 65536 || a->k_heads > 65536)
+    return FP4_E_SHAPE;
+  if (a->head_dim < 16 || a->head_dim > 256 || a->head_dim % 8) return FP4_E_SHAPE;
+  if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 16 || a->table_rows < 0)
+    return FP4_E_SHAPE;
+  if (a->flags & ~(uint32_t)FP4_ROPE_INTERLEAVED) return FP4_E_FLAGS;
+  if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return FP4_E_SHAPE;
+  if (a->tokens == 0 || a->q_heads + a->k_heads == 0) return FP4_OK;
+  if ((a->q_heads && !a->q) || (a->k_heads && !a->k)) return FP4_E_NULL;
+  if (a->rot_dim > 0 && (!a->positions || !a->table)) return FP4_E_NULL;
+  if (a->rot_dim > 0 && a->table_rows == 0) return FP4_E_SHAPE;
+  if (a->q_heads)
+    if (int rc = check_tokens(a->tokens, a->q_stride, (int64_t)a->q_heads * a->head_dim)) return rc;
+  if (a->k_heads)
+    if (int rc = check_tokens(a->tokens, a->k_stride, (int64_t)a->k_heads * a->head_dim)) return rc;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->q_weight, 16) ||
+      !aligned(a->k_weight, 16) || !aligned(a->positions, 8) || !aligned(a->table, 16))
+    return FP4_E_ALIGN;
+  return FP4_OK;
+}
+
+// A second tensor of the same heads (outputs and gradients).
+int check_rope_pair(const fp4_qk_rope* a, const void* q, int64_t qs, const void* k, int64_t ks) {
+  if (a->tokens == 0) return FP4_OK;
+  if ((a->q_heads && !q) || (a->k_heads && !k)) return FP4_E_NULL;
+  if (a->q_heads)
+    if (int rc = check_tokens(a->tokens, qs, (int64_t)a->q_heads * a->head_dim)) return rc;
+  if (a->k_heads)
+    if (int rc = check_tokens(a->tokens, ks, (int64_t)a->k_heads * a->head_dim)) return rc;
+  return aligned(q, 16) && aligned(k, 16) ? FP4_OK : FP4_E_ALIGN;
+}
+
+RopeArgs rope_args(const fp4_qk_rope* a) {
+  RopeArgs r;
+  r.q = a->q;
+  r.k = a->k;
+  r.qw = a->q_weight;
+  r.kw = a->k_weight;
+  r.pos = a->positions;
+  r.table = a->table;
+  r.qs = a->q_stride;
+  r.ks = a->k_stride;
+  r.tokens = a->tokens;
+  r.table_rows = a->table_rows;
+  r.hq = a->q_heads;
+  r.hk = a->k_heads;
+  r.dim = a->head_dim;
+  r.rot = a->rot_dim;
+  r.eps = a->eps;
+  r.hpg = 1;
+  r.chunks = a->q_heads + a->k_heads;
+  return r;
+}
+
+// f(lanes per head, interleaved) with both as compile-time constants.
+template <typename F>
+hipError_t rope_variant(const fp4_qk_rope* a, F&& f) {
+  const bool inter = a->flags & FP4_ROPE_INTERLEAVED;
+  auto pick = [&](auto lph) {
+    return inter ? f(lph, std::true_type{}) : f(lph, std::false_type{});
+  };
+  switch (lanes_per_head(a->head_dim)) {
+    case 2: return pick(std::integral_constant<int, 2>{});
+    case 4: return pick(std::integral_constant<int, 4>{});
+    case 8: return pick(std::integral_constant<int, 8>{});
+    case 16: return pick(std::integral_constant<int, 16>{});
+    default: return pick(std::integral_constant<int, 32>{});
+  }
+}
+
+// Workgroups of the backward pass: the rows of partial weight gradients.
+int64_t rope_bwd_groups(const fp4_qk_rope* a, const RopeArgs& r) {
+  const int64_t per = kRopeThreads / lanes_per_head(a->head_dim);
+  const int64_t g = cdiv(a->tokens * r.chunks, per);
+  return g < 1 ? 1 : (g < kRopeMaxGroups ? g : kRopeMaxGroups);
+}
+
+// ------------------------------------------------------------------ attention
+int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16_t* out,
+                    int64_t out_stride, const float* lse) {
+  if (!x) return FP4_E_NULL;
+  if (int rc = check_kv_cache(c)) return rc;
+  if (x->tokens < 0 || x->tokens >= ((int64_t)1 << 31) || x->seqs < 0 ||
+      x->seqs >= ((int64_t)1 << 31) || x->table_width < 0 || x->max_q < 0 ||
+      x->table_width > (((int64_t)1 << 31) - 1) / c->page_size)
+    return FP4_E_SHAPE;
+  if (x->q_heads < 1 || x->q_heads > 65536 || x->q_heads % c->heads) return FP4_E_SHAPE;
+  if (!x->cu_q && x->tokens != x->seqs) return FP4_E_SHAPE;
+  if (x->window < 0 || !(x->softcap >= 0.0f) || std::isinf(x->softcap) || !std::isfinite(x->scale))
+    return FP4_E_SHAPE;
+  if (x->tokens == 0) return FP4_OK;
+  if (x->seqs == 0) return FP4_E_SHAPE;
+  if (!x->q || !out || !x->kv_lens || (x->table_width > 0 && !x->page_table)) return FP4_E_NULL;
+  const int64_t width = (int64_t)x->q_heads * c->head_dim;
+  if (int rc = check_tokens(x->tokens, x->q_stride, width)) return rc;
+  if (int rc = check_tokens(x->tokens, out_stride, width)) return rc;
+  if (!aligned(x->q, 16) || !aligned(out, 16) || !aligned(x->page_table, 4) ||
+      !aligned(x->kv_lens, 4) || !aligned(x->cu_q, 4) || !aligned(lse, 4))
+    return FP4_E_ALIGN;
+  return FP4_OK;
+}
+
+template <int MODE>
+hipError_t launch_attention(int dim, const AttnArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)cdiv(a.tokens * a.hq, kThreads / 64);
+  switch (dim) {
+    case 64: return launch(kv_attention_kernel<MODE, 64>, grid, kThreads, st, a);
+    case 128: return launch(kv_attention_kernel<MODE, 128>, grid, kThreads, st, a);
+    default: return launch(kv_attention_kernel<MODE, 256>, grid, kThreads, st, a);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk_norm_rope(const fp4_qk_rope* a, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                 int64_t k_out_stride, void* stream) {
+  if (int rc = check_rope(a)) return rc;
+  if (int rc = check_rope_pair(a, q_out, q_out_stride, k_out, k_out_stride)) return rc;
+  if (a->tokens == 0 || a->q_heads + a->k_heads == 0) return FP4_OK;
+  const RopeArgs r = rope_args(a);
+  return launched(rope_variant(a, [&](auto lph, auto inter) {
+    constexpr int L = decltype(lph)::value;
+    return launch(qk_norm_rope_kernel<L, decltype(inter)::value>,
+                  (unsigned)cdiv(r.tokens * r.chunks, kRopeThreads / L), kRopeThreads,
+                  (hipStream_t)stream, r, q_out, q_out_stride, k_out, k_out_stride);
+  }));
+}
+
+size_t qk_norm_rope_workspace_bytes(int head_dim) {
+  if (head_dim < 16 || head_dim > 256) return 0;
+  return (size_t)kRopeMaxGroups * 2 * (size_t)head_dim * sizeof(float);
+}
+
+int qk_norm_rope_backward(const fp4_qk_rope* a, const uint16_t* dq_out, int64_t dq_out_stride,
+                          const uint16_t* dk_out, int64_t dk_out_stride, uint16_t* dq,
+                          int64_t dq_stride, uint16_t* dk, int64_t dk_stride, float* dq_weight,
+                          float* dk_weight, void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_rope(a)) return rc;
+  if (int rc = check_rope_pair(a, dq_out, dq_out_stride, dk_out, dk_out_stride)) return rc;
+  if (int rc = check_rope_pair(a, dq, dq_stride, dk, dk_stride)) return rc;
+  const bool want_w = dq_weight || dk_weight;
+  if ((dq_weight && !a->q_weight) || (dk_weight && !a->k_weight)) return FP4_E_NULL;
+  if (want_w && !ws) return FP4_E_NULL;
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(ws, 4)) return FP4_E_ALIGN;
+  if (want_w && ws_bytes < qk_norm_rope_workspace_bytes(a->head_dim)) return FP4_E_WORKSPACE;
+  const RopeArgs r = rope_args(a);
+  const bool none = a->tokens == 0 || a->q_heads + a->k_heads == 0;
+  if (none && !want_w) return FP4_OK;
+  hipStream_t st = (hipStream_t)stream;
+  const int64_t groups = none ? 0 : rope_bwd_groups(a, r);
+  hipError_t e = hipSuccess;
+  if (!none)
+    e = rope_variant(a, [&](auto lph, auto inter) {
+      return launch(qk_norm_rope_bwd_kernel<decltype(lph)::value, decltype(inter)::value>,
+                    (unsigned)groups, kRopeThreads, st, r, dq_out, dq_out_stride, dk_out,
+                    dk_out_stride, dq, dq_stride, dk, dk_stride, want_w ? (float*)ws : nullptr);
+    });
+  if (want_w)
+    e = first(e, launch(qk_norm_rope_dw_kernel, (unsigned)cdiv(2 * a->head_dim, 16), kRopeThreads,
+                        st, (const float*)ws, (int)groups, a->head_dim, dq_weight, dk_weight));
+  return launched(e);
+}
+
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_queries* x) {
+  (void)cache; (void)x;
+  return 0;
+}
+
+int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* out,
+                     int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_attention(c, x, out, out_stride, lse)) return rc;
+  if (!aligned(ws, 16)) return FP4_E_ALIGN;
+  if (ws_bytes < fp4_kv_attention_workspace_bytes(c, x)) return FP4_E_WORKSPACE;
+  if (x->tokens == 0) return FP4_OK;
+  AttnArgs a;
+  a.c = kv_view(c);
+  a.q = x->q;
+  a.pt = x->page_table;
+  a.lens = x->kv_lens;
+  a.cu = x->cu_q;
+  a.out = out;
+  a.lse = lse;
+  a.qs = x->q_stride;
+  a.os = out_stride;
+  a.tokens = x->tokens;
+  a.seqs = x->seqs;
+  a.width = x->table_width;
+  a.hq = x->q_heads;
+  a.group = x->q_heads / c->heads;
+  a.window = x->window;
+  a.scale = x->scale;
+  a.cap = x->softcap;
+  hipStream_t st = (hipStream_t)stream;
+  switch (kv_mode(c)) {
+    case 0: return launched(launch_attention<0>(c->head_dim, a, st));
+    case 1: return launched(launch_attention<1>(c->head_dim, a, st));
+    default: return launched(launch_attention<2>(c->head_dim, a, st));
+  }
+}
+
+}  // extern "C"

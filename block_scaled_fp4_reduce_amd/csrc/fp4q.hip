@@ -6,6 +6,9 @@
 #include <mutex>
 
 #include "../../include/fp4q.h"
+#include "host_common.h"
+#include "kv_cache_kernels.h"
+#include "kv_host.h"
 #include "msed_kernels.h"
 #include "mxgemm_kernels.h"
 #include "mx_kernels.h"
@@ -26,14 +29,9 @@ static __device__ __align__(256) uint32_t scratch[kScratchBytes / sizeof(uint32_
 
 namespace {
 
-constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr uint32_t kNvfp4Flags = FP4_FOUR_OVER_SIX | FP4_SR | FP4_RHT16 | FP4_BLOCK2D |
                                  FP4_ROWWISE | FP4_COLWISE | FP4_MSEDEN;
 constexpr uint32_t kMxFlags = FP4_HAD32 | FP4_ROWWISE | FP4_COLWISE;
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int check_shape(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0) return FP4_E_SHAPE;
@@ -66,27 +64,6 @@ int amax_groups(int64_t ngroups16, bool one_d) {
   if (g < 1) g = 1;
   if (g > cap) g = cap;
   return (int)g;
-}
-
-// Status of the launches an entry point queued (each launch reports its own
-// result, see launch(); the thread's last-error state is never read).
-int launched(hipError_t e) { return e == hipSuccess ? FP4_OK : FP4_E_HIP; }
-
-// First failure of a sequence of launches.
-hipError_t first(hipError_t a, hipError_t b) { return a != hipSuccess ? a : b; }
-
-// Compute units of the current device (queried once per device; 256 on MI355X).
-int num_cus() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-      n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 // Queue the amax pass: partial maxima into ws (as uint32), `groups` of them.
@@ -508,6 +485,64 @@ int fp4_dequantize(int format, const uint8_t* codes, const uint8_t* scales, cons
   const int64_t ng = n / 32;
   return launched(launch(mxfp4_dequant_kernel, (unsigned)cdiv(ng, kThreads), kThreads, st,
                          (const uint4*)codes, scales, ng, (float4*)out));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Tokens of an fp4_kv_write or fp4_kv_read: rows of heads * head_dim values.
+int check_kv_tokens(const fp4_kv_cache* c, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const int64_t* slots, int64_t tokens) {
+  if (int rc = check_kv_cache(c)) return rc;
+  const int64_t width = (int64_t)c->heads * c->head_dim;
+  if (tokens < 0 || tokens >= kMaxElems / (2 * width)) return FP4_E_SHAPE;
+  if (tokens == 0) return FP4_OK;
+  if (!k || !v || !slots) return FP4_E_NULL;
+  for (int64_t s : {k_stride, v_stride})
+    if (s < width || s % 8 || s > kMaxElems / tokens) return FP4_E_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return FP4_E_ALIGN;
+  return FP4_OK;
+}
+
+// Workgroups of one lane per group of G values of every key and value.
+int64_t kv_lane_grid(const fp4_kv_cache* c, int64_t tokens) {
+  const int G = c->format == FP4_FORMAT_MXFP4 ? 32 : 16;
+  return cdiv(tokens * 2 * c->heads * (c->head_dim / G), kThreads);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp4_kv_write(const fp4_kv_cache* c, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                 int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream) {
+  if (int rc = check_kv_tokens(c, k, k_stride, v, v_stride, slots, tokens)) return rc;
+  if (tokens == 0 || c->pages == 0) return FP4_OK;
+  const int64_t grid = kv_lane_grid(c, tokens);
+  if (grid >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
+  const KvView view = kv_view(c);
+  hipStream_t st = (hipStream_t)stream;
+#define FP4Q_KV(M) launched(launch(kv_write_kernel<M>, (unsigned)grid, kThreads, st, view, k, \
+                                   k_stride, v, v_stride, slots, tokens))
+  const int mode = kv_mode(c);
+  return mode == 0 ? FP4Q_KV(0) : (mode == 1 ? FP4Q_KV(1) : FP4Q_KV(2));
+#undef FP4Q_KV
+}
+
+int fp4_kv_read(const fp4_kv_cache* c, const int64_t* slots, int64_t tokens, uint16_t* k,
+                int64_t k_stride, uint16_t* v, int64_t v_stride, void* stream) {
+  if (int rc = check_kv_tokens(c, k, k_stride, v, v_stride, slots, tokens)) return rc;
+  if (tokens == 0) return FP4_OK;
+  const int64_t grid = kv_lane_grid(c, tokens);
+  if (grid >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
+  const KvView view = kv_view(c);
+  hipStream_t st = (hipStream_t)stream;
+#define FP4Q_KV(M) launched(launch(kv_read_kernel<M>, (unsigned)grid, kThreads, st, view, slots, \
+                                   tokens, k, k_stride, v, v_stride))
+  const int mode = kv_mode(c);
+  return mode == 0 ? FP4Q_KV(0) : (mode == 1 ? FP4Q_KV(1) : FP4Q_KV(2));
+#undef FP4Q_KV
 }
 
 }  // extern "C"

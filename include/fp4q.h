@@ -57,7 +57,8 @@ typedef enum {
   FP4_OK = 0,
   FP4_E_NULL = -1,      /* a required pointer is NULL                     */
   FP4_E_SHAPE = -2,     /* rows/cols negative, not a block multiple, or
-                           rows*cols >= 2^40                              */
+                           rows*cols >= 2^40; a size or number out of the
+                           range that its call names                      */
   FP4_E_ALIGN = -3,     /* a pointer breaks the alignment rules above     */
   FP4_E_FLAGS = -4,     /* unknown bit or an unsupported combination      */
   FP4_E_WORKSPACE = -5, /* workspace smaller than fp4_workspace_bytes()   */
@@ -256,6 +257,134 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b
 int fp4_dequantize(int format, const uint8_t* codes, const uint8_t* scales,
                    const float* alpha, int64_t rows, int64_t cols,
                    uint32_t flags, float* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over a paged FP4 key/value cache, and the norm with rotation
+ * that makes its queries and keys.
+ *
+ * Queries, keys, values, their outputs and gradients are bf16
+ * [tokens][heads][head_dim]: a token's heads are contiguous, `*_stride` is
+ * the number of elements from one token to the next (a multiple of 8, at
+ * least heads * head_dim), so slices of a fused projection need no copy.
+ * Pointers are 16-byte aligned.  The structs are read by the call itself and
+ * need not outlive it.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache of keys and values in FP4, in the caller's memory.  With
+ * page size P, G = 16 (NVFP4) or 32 (MXFP4):
+ *   k_codes  [pages][heads][P][head_dim/2]   two codes per byte, even low
+ *   k_scales [pages][heads][P][head_dim/G]
+ *   v_codes  [pages][heads][head_dim/2][P]   the same bytes, tokens innermost
+ *   v_scales [pages][heads][head_dim/G][P]
+ * Slot s is token s % P of page s / P.  Every head is quantized along
+ * head_dim as nvfp4_quantize (flags FP4_RTN6 or FP4_FOUR_OVER_SIX, the
+ * head's largest magnitude given as amax_in) or mxfp4_quantize would;
+ * magnitudes past the given one saturate. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_amax;   /* [heads] device floats, NVFP4 only (else NULL)     */
+  const float* v_amax;
+  int64_t pages;
+  int32_t page_size;     /* a power of two, 16 to 4096                        */
+  int32_t heads;
+  int32_t head_dim;      /* 64, 128 or 256                                    */
+  int32_t format;        /* FP4_FORMAT_NVFP4 or FP4_FORMAT_MXFP4              */
+  uint32_t flags;        /* NVFP4: FP4_RTN6 or FP4_FOUR_OVER_SIX; MXFP4: 0    */
+} fp4_kv_cache;
+
+/* Quantize the keys and values of `tokens` tokens into the cache at `slots`
+ * [tokens] (int64).  A slot outside the cache is skipped; slots of one call
+ * are distinct (of equal ones an unspecified mixture is kept). */
+int fp4_kv_write(const fp4_kv_cache* cache, const uint16_t* k, int64_t k_stride,
+                 const uint16_t* v, int64_t v_stride, const int64_t* slots, int64_t tokens,
+                 void* stream);
+
+/* Read the keys and values at `slots` back: q * (alpha * Delta), or
+ * q * 2^(code-127), rounded to bf16.  A slot outside the cache reads as 0. */
+int fp4_kv_read(const fp4_kv_cache* cache, const int64_t* slots, int64_t tokens, uint16_t* k,
+                int64_t k_stride, uint16_t* v, int64_t v_stride, void* stream);
+
+/* New tokens that attend over the cache.  Token i of a sequence's n stands
+ * at position kv_len - n + i (its own key is already in the cache) and sees
+ * the positions up to its own, with a window W the last W of them.  Position
+ * j of sequence b is token j % P of page page_table[b][j / P]. */
+typedef struct {
+  const uint16_t* q;           /* [tokens][q_heads][head_dim]                 */
+  int64_t q_stride;
+  int64_t tokens;              /* new tokens of all sequences                 */
+  int64_t seqs;
+  const int32_t* cu_q;         /* [seqs + 1] first token of each sequence,
+                                  cu_q[seqs] = tokens; NULL: one token each   */
+  int64_t max_q;               /* at least every sequence's number of new
+                                  tokens; 0: not known                        */
+  const int32_t* kv_lens;      /* [seqs] cached tokens, the new ones included */
+  const int32_t* page_table;   /* [seqs][table_width]                         */
+  int64_t table_width;
+  int32_t q_heads;             /* a multiple of the cache's heads; query head
+                                  h reads kv head h / (q_heads / heads)       */
+  int32_t window;              /* 0: none                                     */
+  float scale;                 /* of the scores, usually head_dim^-1/2        */
+  float softcap;               /* c > 0: scores become c tanh(s / c); 0: none */
+} fp4_kv_queries;
+
+/* Device workspace of fp4_kv_attention for these sizes (needs no
+ * initialisation; may be 0). */
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_queries* x);
+
+/* out = softmax(scores) V over the cached tokens that each new token sees,
+ * bf16 [tokens][q_heads][head_dim]; lse NULL or [tokens][q_heads] floats,
+ * the log of the sum of the scores' exponentials.  A token that sees
+ * nothing (kv_len 0, or fewer cached tokens than new ones) gets out = 0 and
+ * lse = -inf.  Cached bytes past a sequence's length are never looked at,
+ * whatever they hold; a page id outside the cache contributes nothing; a
+ * length past the table is cut to it. */
+int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_queries* x, uint16_t* out,
+                     int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+enum { FP4_ROPE_INTERLEAVED = 1u << 0 };   /* pairs (2i, 2i+1) instead of (i, i + rot/2) */
+
+/* Queries and keys for the norm with rotation.  Per head of a token at
+ * position p:  y = R_p (x / sqrt(mean(x^2) + eps) * weight), R_p rotating
+ * pair i of the first rot_dim values by the angle whose cosine and sine are
+ * table[p][i]; the other values pass. */
+typedef struct {
+  const uint16_t* q;           /* [tokens][q_heads][head_dim]; NULL with q_heads 0 */
+  const uint16_t* k;           /* [tokens][k_heads][head_dim]; NULL with k_heads 0 */
+  int64_t q_stride, k_stride;
+  int64_t tokens;
+  const uint16_t* q_weight;    /* [head_dim] bf16; NULL: no norm of the queries */
+  const uint16_t* k_weight;
+  const int64_t* positions;    /* [tokens], in [0, table_rows)                */
+  const float* table;          /* [table_rows][rot_dim/2][2]: cosine, sine
+                                  (neither is looked at with rot_dim 0)       */
+  int64_t table_rows;
+  int32_t q_heads, k_heads;
+  int32_t head_dim;            /* a multiple of 8, 16 to 256                  */
+  int32_t rot_dim;             /* a multiple of 16, at most head_dim          */
+  float eps;
+  uint32_t flags;              /* FP4_ROPE_INTERLEAVED or 0                   */
+} fp4_qk_rope;
+
+/* Forward.  q_out may be q and k_out may be k (with the same strides).
+ * Positions outside the table take its nearest row. */
+int qk_norm_rope(const fp4_qk_rope* x, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                 int64_t k_out_stride, void* stream);
+
+/* Bytes of device workspace of the backward pass (no initialisation). */
+size_t qk_norm_rope_workspace_bytes(int head_dim);
+
+/* Backward: from the gradients of the outputs (dq_out, dk_out) and the
+ * forward's inputs, the gradients of q, k (bf16) and of the weights (fp32
+ * [head_dim], NULL where not wanted; summed over tokens and heads in an
+ * order that depends on the sizes alone).  ws may be NULL without weight
+ * gradients.  dq may be dq_out and dk may be dk_out. */
+int qk_norm_rope_backward(const fp4_qk_rope* x, const uint16_t* dq_out, int64_t dq_out_stride,
+                          const uint16_t* dk_out, int64_t dk_out_stride, uint16_t* dq,
+                          int64_t dq_stride, uint16_t* dk, int64_t dk_stride, float* dq_weight,
+                          float* dk_weight, void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* fp4_status_str(int status);
