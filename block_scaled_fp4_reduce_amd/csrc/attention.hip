@@ -109,8 +109,7 @@ int64_t rope_bwd_groups(const fp4_qk_rope* a, const RopeArgs& r) {
 }
 
 // ------------------------------------------------------------------ attention
-int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16_t* out,
-                    int64_t out_stride, const float* lse) {
+int check_attention_sizes(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   if (!x) return FP4_E_NULL;
   if (int rc = check_kv_cache(c)) return rc;
   if (x->tokens < 0 || x->tokens >= ((int64_t)1 << 31) || x->seqs < 0 ||
@@ -121,8 +120,13 @@ int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16
   if (!x->cu_q && x->tokens != x->seqs) return FP4_E_SHAPE;
   if (x->window < 0 || !(x->softcap >= 0.0f) || std::isinf(x->softcap) || !std::isfinite(x->scale))
     return FP4_E_SHAPE;
+  return x->tokens > 0 && x->seqs == 0 ? FP4_E_SHAPE : FP4_OK;
+}
+
+int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16_t* out,
+                    int64_t out_stride, const float* lse) {
+  if (int rc = check_attention_sizes(c, x)) return rc;
   if (x->tokens == 0) return FP4_OK;
-  if (x->seqs == 0) return FP4_E_SHAPE;
   if (!x->q || !out || !x->kv_lens || (x->table_width > 0 && !x->page_table)) return FP4_E_NULL;
   const int64_t width = (int64_t)x->q_heads * c->head_dim;
   if (int rc = check_tokens(x->tokens, x->q_stride, width)) return rc;
@@ -133,13 +137,59 @@ int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16
   return FP4_OK;
 }
 
+// How a call is cut up: columns of 16 rows per tile, tiles of the grid (an
+// upper bound of what the sequences need), parts of the context.
+struct AttnPlan {
+  int nt, waves;
+  int64_t tiles, splits;
+};
+
+AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
+  AttnPlan p;
+  const int64_t group = x->q_heads / c->heads;
+  const int64_t most = !x->cu_q ? 1 : (x->max_q > 0 ? x->max_q : cdiv(x->tokens, x->seqs));
+  const int64_t rows = most * group;
+  p.nt = rows <= 16 || c->head_dim == 256 ? 1 : 2;
+  p.waves = 4;
+  const int64_t m = 16 * p.nt;
+  p.tiles = x->cu_q ? x->tokens * group / m + x->seqs : x->seqs * cdiv(group, m);
+  // keys in reach of a tile, at most
+  int64_t keys = x->table_width * c->page_size;
+  if (x->window > 0 && keys > x->window + most) keys = x->window + most;
+  const int64_t blocks = cdiv(keys, kAttnKeys);
+  const int64_t want = cdiv(4 * (int64_t)num_cus() * 4, p.tiles * c->heads * p.waves);
+  const int64_t room = cdiv(blocks, p.waves);
+  p.splits = want < room ? want : room;
+  p.splits = p.splits < 1 ? 1 : (p.splits > 64 ? 64 : p.splits);
+  return p;
+}
+
+size_t attention_ws(const fp4_kv_cache* c, const fp4_kv_queries* x, const AttnPlan& p) {
+  if (p.splits <= 1) return 0;
+  return (size_t)p.splits * x->tokens * x->q_heads * (c->head_dim + 2) * sizeof(float);
+}
+
+template <int MODE, int D>
+hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)(p.tiles * p.splits * a.c.heads);
+  hipError_t e = hipSuccess;
+  if (p.nt == 1) {
+    e = launch(kv_attention_kernel<MODE, D, 1, 4>, grid, 256, st, a);
+  } else {
+    if constexpr (D < 256) e = launch(kv_attention_kernel<MODE, D, 2, 4>, grid, 256, st, a);
+  }
+  if (p.splits > 1)
+    e = first(e, launch(kv_attention_join_kernel<MODE, D>,
+                        (unsigned)cdiv(a.tokens * a.hq, kThreads / 64), kThreads, st, a));
+  return e;
+}
+
 template <int MODE>
-hipError_t launch_attention(int dim, const AttnArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)cdiv(a.tokens * a.hq, kThreads / 64);
+hipError_t launch_attention(int dim, const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
   switch (dim) {
-    case 64: return launch(kv_attention_kernel<MODE, 64>, grid, kThreads, st, a);
-    case 128: return launch(kv_attention_kernel<MODE, 128>, grid, kThreads, st, a);
-    default: return launch(kv_attention_kernel<MODE, 256>, grid, kThreads, st, a);
+    case 64: return launch_attention<MODE, 64>(p, a, st);
+    case 128: return launch_attention<MODE, 128>(p, a, st);
+    default: return launch_attention<MODE, 256>(p, a, st);
   }
 }
 
@@ -197,16 +247,20 @@ int qk_norm_rope_backward(const fp4_qk_rope* a, const uint16_t* dq_out, int64_t 
 }
 
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_queries* x) {
-  (void)cache; (void)x;
-  return 0;
+  if (check_attention_sizes(cache, x) || x->tokens == 0) return 0;
+  return attention_ws(cache, x, attention_plan(cache, x));
 }
 
 int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* out,
                      int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (int rc = check_attention(c, x, out, out_stride, lse)) return rc;
   if (!aligned(ws, 16)) return FP4_E_ALIGN;
-  if (ws_bytes < fp4_kv_attention_workspace_bytes(c, x)) return FP4_E_WORKSPACE;
   if (x->tokens == 0) return FP4_OK;
+  const AttnPlan p = attention_plan(c, x);
+  if (p.tiles > (((int64_t)1 << 32) - 1) / kThreads / p.splits / c->heads) return FP4_E_SHAPE;
+  const size_t need = attention_ws(c, x, p);
+  if (need > 0 && !ws) return FP4_E_NULL;
+  if (ws_bytes < need) return FP4_E_WORKSPACE;
   AttnArgs a;
   a.c = kv_view(c);
   a.q = x->q;
@@ -225,11 +279,14 @@ int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* o
   a.window = x->window;
   a.scale = x->scale;
   a.cap = x->softcap;
+  a.splits = (int)p.splits;
+  a.po = (float*)ws;
+  a.pm = a.po + (need ? p.splits * x->tokens * x->q_heads * c->head_dim : 0);
   hipStream_t st = (hipStream_t)stream;
   switch (kv_mode(c)) {
-    case 0: return launched(launch_attention<0>(c->head_dim, a, st));
-    case 1: return launched(launch_attention<1>(c->head_dim, a, st));
-    default: return launched(launch_attention<2>(c->head_dim, a, st));
+    case 0: return launched(launch_attention<0>(c->head_dim, p, a, st));
+    case 1: return launched(launch_attention<1>(c->head_dim, p, a, st));
+    default: return launched(launch_attention<2>(c->head_dim, p, a, st));
   }
 }
 
