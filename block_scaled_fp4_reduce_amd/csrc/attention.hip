@@ -8,6 +8,7 @@
 #include "host_common.h"
 #include "kv_attention_kernels.h"
 #include "kv_host.h"
+#include "kv_tiled_kernels.h"
 #include "rope_kernels.h"
 
 using namespace fp4q;
@@ -137,10 +138,11 @@ int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16
   return FP4_OK;
 }
 
-// How a call is cut up: columns of 16 rows per tile, tiles of the grid (an
-// upper bound of what the sequences need), parts of the context.
+// How a call is cut up: columns of 16 rows per tile (0: the tiled kernel),
+// tiles of the grid (an upper bound of what the sequences need), parts of the
+// context.
 struct AttnPlan {
-  int nt, waves;
+  int nt;
   int64_t tiles, splits;
 };
 
@@ -149,16 +151,15 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   const int64_t group = x->q_heads / c->heads;
   const int64_t most = !x->cu_q ? 1 : (x->max_q > 0 ? x->max_q : cdiv(x->tokens, x->seqs));
   const int64_t rows = most * group;
-  p.nt = rows <= 16 || c->head_dim == 256 ? 1 : 2;
-  p.waves = 4;
-  const int64_t m = 16 * p.nt;
+  p.nt = rows <= 16 ? 1 : (rows <= 32 && c->head_dim < 256 ? 2 : 0);
+  const int64_t m = p.nt ? 16 * p.nt : kTileRows;
   p.tiles = x->cu_q ? x->tokens * group / m + x->seqs : x->seqs * cdiv(group, m);
   // keys in reach of a tile, at most
   int64_t keys = x->table_width * c->page_size;
   if (x->window > 0 && keys > x->window + most) keys = x->window + most;
   const int64_t blocks = cdiv(keys, kAttnKeys);
-  const int64_t want = cdiv(4 * (int64_t)num_cus() * 4, p.tiles * c->heads * p.waves);
-  const int64_t room = cdiv(blocks, p.waves);
+  const int64_t want = cdiv(num_cus() * (p.nt ? 4 : 2), p.tiles * c->heads);
+  const int64_t room = cdiv(blocks, 4);
   p.splits = want < room ? want : room;
   p.splits = p.splits < 1 ? 1 : (p.splits > 64 ? 64 : p.splits);
   return p;
@@ -173,7 +174,9 @@ template <int MODE, int D>
 hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)(p.tiles * p.splits * a.c.heads);
   hipError_t e = hipSuccess;
-  if (p.nt == 1) {
+  if (p.nt == 0) {
+    e = launch(kv_tiled_kernel<MODE, D>, grid, kThreads, st, a, (uint32_t)p.tiles);
+  } else if (p.nt == 1) {
     e = launch(kv_attention_kernel<MODE, D, 1, 4>, grid, 256, st, a);
   } else {
     if constexpr (D < 256) e = launch(kv_attention_kernel<MODE, D, 2, 4>, grid, 256, st, a);
