@@ -81,8 +81,13 @@ RopeArgs rope_args(const fp4_qk_rope* a) {
   r.dim = a->head_dim;
   r.rot = a->rot_dim;
   r.eps = a->eps;
-  r.hpg = 1;
-  r.chunks = a->q_heads + a->k_heads;
+  // heads per lane group: more share one read of the token's cosines, fewer
+  // keep every CU supplied with small calls
+  const int64_t heads = a->q_heads + a->k_heads;
+  const int64_t groups = (int64_t)num_cus() * 8 * (64 / lanes_per_head(a->head_dim));
+  const int64_t hpg = heads ? a->tokens * heads / groups : 1;
+  r.hpg = (int)(hpg < 1 ? 1 : (hpg > 8 ? 8 : hpg));
+  r.chunks = (int)cdiv(heads, r.hpg);
   return r;
 }
 
@@ -181,9 +186,15 @@ hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st
   } else {
     if constexpr (D < 256) e = launch(kv_attention_kernel<MODE, D, 2, 4>, grid, 256, st, a);
   }
-  if (p.splits > 1)
+  if (p.splits > 1) {
+    // as many lanes on a row's parts as keep a lane at 4 of them
+    const int lanes = D / 4, most = kThreads / lanes;
+    int parts = 1;
+    while (parts < most && parts * 4 < p.splits) parts *= 2;
     e = first(e, launch(kv_attention_join_kernel<MODE, D>,
-                        (unsigned)cdiv(a.tokens * a.hq, kThreads / 64), kThreads, st, a));
+                        (unsigned)cdiv(a.tokens * a.hq, kThreads / (lanes * parts)), kThreads, st,
+                        a, parts));
+  }
   return e;
 }
 
@@ -244,7 +255,7 @@ int qk_norm_rope_backward(const fp4_qk_rope* a, const uint16_t* dq_out, int64_t 
                     dk_out_stride, dq, dq_stride, dk, dk_stride, want_w ? (float*)ws : nullptr);
     });
   if (want_w)
-    e = first(e, launch(qk_norm_rope_dw_kernel, (unsigned)cdiv(2 * a->head_dim, 16), kRopeThreads,
+    e = first(e, launch(qk_norm_rope_dw_kernel, (unsigned)cdiv(2 * a->head_dim, kDwCols), kDwThreads,
                         st, (const float*)ws, (int)groups, a->head_dim, dq_weight, dk_weight));
   return launched(e);
 }

@@ -505,10 +505,31 @@ int check_kv_tokens(const fp4_kv_cache* c, const void* k, int64_t k_stride, cons
   return FP4_OK;
 }
 
-// Workgroups of one lane per group of G values of every key and value.
-int64_t kv_lane_grid(const fp4_kv_cache* c, int64_t tokens) {
-  const int G = c->format == FP4_FORMAT_MXFP4 ? 32 : 16;
-  return cdiv(tokens * 2 * c->heads * (c->head_dim / G), kThreads);
+// f(mode, head_dim, tokens per workgroup) as compile-time constants, with the
+// grid of that tile.  64 tokens fill the 64-byte lines of a page's rows of
+// values; with too few tiles of 64 for the CUs, tiles of 16 spread the call
+// over more of them.
+template <typename F>
+int kv_variant(const fp4_kv_cache* c, int64_t tokens, F&& f) {
+  const int64_t tt = cdiv(tokens, 64) * c->heads >= 2 * num_cus() ? 64 : 16;
+  const int64_t grid = cdiv(tokens, tt) * c->heads;
+  if (grid > (((int64_t)1 << 32) - 1) / kThreads) return FP4_E_SHAPE;
+  auto tile = [&](auto mode, auto dim) {
+    return tt == 64 ? f(mode, dim, std::integral_constant<int, 64>{}, (unsigned)grid)
+                    : f(mode, dim, std::integral_constant<int, 16>{}, (unsigned)grid);
+  };
+  auto head = [&](auto mode) {
+    switch (c->head_dim) {
+      case 64: return tile(mode, std::integral_constant<int, 64>{});
+      case 128: return tile(mode, std::integral_constant<int, 128>{});
+      default: return tile(mode, std::integral_constant<int, 256>{});
+    }
+  };
+  switch (kv_mode(c)) {
+    case 0: return launched(head(std::integral_constant<int, 0>{}));
+    case 1: return launched(head(std::integral_constant<int, 1>{}));
+    default: return launched(head(std::integral_constant<int, 2>{}));
+  }
 }
 
 }  // namespace
@@ -519,30 +540,22 @@ int fp4_kv_write(const fp4_kv_cache* c, const uint16_t* k, int64_t k_stride, con
                  int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream) {
   if (int rc = check_kv_tokens(c, k, k_stride, v, v_stride, slots, tokens)) return rc;
   if (tokens == 0 || c->pages == 0) return FP4_OK;
-  const int64_t grid = kv_lane_grid(c, tokens);
-  if (grid >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
-  const KvView view = kv_view(c);
-  hipStream_t st = (hipStream_t)stream;
-#define FP4Q_KV(M) launched(launch(kv_write_kernel<M>, (unsigned)grid, kThreads, st, view, k, \
-                                   k_stride, v, v_stride, slots, tokens))
-  const int mode = kv_mode(c);
-  return mode == 0 ? FP4Q_KV(0) : (mode == 1 ? FP4Q_KV(1) : FP4Q_KV(2));
-#undef FP4Q_KV
+  return kv_variant(c, tokens, [&](auto mode, auto dim, auto tt, unsigned grid) {
+    return launch(kv_write_kernel<decltype(mode)::value, decltype(dim)::value, decltype(tt)::value>,
+                  grid, kThreads, (hipStream_t)stream, kv_view(c), k, k_stride, v, v_stride, slots,
+                  tokens);
+  });
 }
 
 int fp4_kv_read(const fp4_kv_cache* c, const int64_t* slots, int64_t tokens, uint16_t* k,
                 int64_t k_stride, uint16_t* v, int64_t v_stride, void* stream) {
   if (int rc = check_kv_tokens(c, k, k_stride, v, v_stride, slots, tokens)) return rc;
   if (tokens == 0) return FP4_OK;
-  const int64_t grid = kv_lane_grid(c, tokens);
-  if (grid >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
-  const KvView view = kv_view(c);
-  hipStream_t st = (hipStream_t)stream;
-#define FP4Q_KV(M) launched(launch(kv_read_kernel<M>, (unsigned)grid, kThreads, st, view, slots, \
-                                   tokens, k, k_stride, v, v_stride))
-  const int mode = kv_mode(c);
-  return mode == 0 ? FP4Q_KV(0) : (mode == 1 ? FP4Q_KV(1) : FP4Q_KV(2));
-#undef FP4Q_KV
+  return kv_variant(c, tokens, [&](auto mode, auto dim, auto tt, unsigned grid) {
+    return launch(kv_read_kernel<decltype(mode)::value, decltype(dim)::value, decltype(tt)::value>,
+                  grid, kThreads, (hipStream_t)stream, kv_view(c), slots, tokens, k, k_stride, v,
+                  v_stride);
+  });
 }
 
 }  // extern "C"

@@ -582,42 +582,54 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
   }
 }
 
-// Joins the parts of the context: one wave per query row.
+// Joins the parts of the context: D/4 lanes (16 bytes each) times `parts`
+// (a power of two) for a query row, the parts taking the splits in turn.
 template <int MODE, int D>
-__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int parts) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f;
-  constexpr int VPL = D / 64;
-  const int lane = (int)threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  constexpr int L = D / 4;
+  __shared__ float4 sx[kThreads];
+  __shared__ float2 sm[kThreads];
+  const int t = (int)threadIdx.x, lane = t % L, part = t / L % parts;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / (L * parts)) + t / (L * parts);
   const int64_t rows = a.tokens * a.hq;
-  if (row >= rows) return;
+  const bool live = row < rows;
+  float top = -__builtin_inff(), l = 0.0f, x[4] = {};
+  auto add = [&](float m1, float l1, float4 y) {
+    const float mm = fmaxf(top, m1);
+    const float f0 = top == mm ? 1.0f : __builtin_amdgcn_exp2f(top - mm);
+    const float f1 = m1 == mm ? 1.0f : __builtin_amdgcn_exp2f(m1 - mm);
+    l = l * f0 + l1 * f1;
+    x[0] = x[0] * f0 + y.x * f1;
+    x[1] = x[1] * f0 + y.y * f1;
+    x[2] = x[2] * f0 + y.z * f1;
+    x[3] = x[3] * f0 + y.w * f1;
+    top = mm;
+  };
+  if (live) {
+#pragma unroll 4
+    for (int s = part; s < a.splits; s += parts) {
+      const float2 ml = *(const float2*)(a.pm + (s * rows + row) * 2);
+      const float4 y = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
+      add(ml.x, ml.y, y);
+    }
+  }
+  if (parts > 1) {
+    for (int half = parts / 2; half > 0; half >>= 1) {
+      __syncthreads();
+      sx[t] = make_float4(x[0], x[1], x[2], x[3]);
+      sm[t] = make_float2(top, l);
+      __syncthreads();
+      if (part < half) add(sm[t + half * L].x, sm[t + half * L].y, sx[t + half * L]);
+    }
+  }
+  if (!live || part) return;
   const int64_t tok = row / a.hq;
   const int head = (int)(row - tok * a.hq), h = head / a.group;
-  float top = -__builtin_inff(), l = 0.0f, x[VPL] = {};
-  for (int s = 0; s < a.splits; s++) {
-    const float2 ml = *(const float2*)(a.pm + (s * rows + row) * 2);
-    const float* p = a.po + (s * rows + row) * D + lane * VPL;
-    float y[VPL];
-#pragma unroll
-    for (int e = 0; e < VPL; e++) y[e] = p[e];
-    const float mm = fmaxf(top, ml.x);
-    const float f0 = top == mm ? 1.0f : __builtin_amdgcn_exp2f(top - mm);
-    const float f1 = ml.x == mm ? 1.0f : __builtin_amdgcn_exp2f(ml.x - mm);
-    l = l * f0 + ml.y * f1;
-#pragma unroll
-    for (int e = 0; e < VPL; e++) x[e] = x[e] * f0 + y[e] * f1;
-    top = mm;
-  }
   const float va = MODE == 2 ? 1.0f : a.c.vam[h] / (6.0f * (MODE == 1 ? 256.0f : 448.0f));
   const float inv = l == 0.0f ? 0.0f : va / l;
-  uint16_t* o = a.out + tok * a.os + (int64_t)head * D + lane * VPL;
-  if constexpr (VPL == 1) {
-    o[0] = (uint16_t)bf16x2_of(x[0] * inv, 0.0f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VPL; e += 2)
-      *(uint32_t*)(o + e) = bf16x2_of(x[e] * inv, x[e + 1] * inv);
-  }
+  *(uint2*)(a.out + tok * a.os + (int64_t)head * D + lane * 4) =
+      make_uint2(bf16x2_of(x[0] * inv, x[1] * inv), bf16x2_of(x[2] * inv, x[3] * inv));
   if (a.lse && lane == 0)
     a.lse[row] = l == 0.0f ? -__builtin_inff() : __builtin_fmaf(top - kOff, kLn2, logf(l));
 }

@@ -58,89 +58,181 @@ __device__ __forceinline__ void kv_quant32(const float* y, uint32_t* w, uint32_t
 template <int MODE>
 constexpr int kv_group() { return MODE == 2 ? 32 : 16; }
 
-// One lane per group of one head's key or value (the first half of the
-// lanes of a token take its keys).
-template <int MODE>
+// Both kernels: a workgroup takes TT consecutive tokens of one head.  Keys go
+// straight through: a token's codes are one run, as its values are.  A
+// value's tokens are a run for each pair of channels, so values are turned in
+// LDS, and where 16 tokens in a row sit side by side in their page (a prompt
+// stored or read in order) a lane moves all 16 bytes of a channel pair at
+// once; otherwise byte by byte.
+//
+// Slots of the tile, and which of its 16-token stretches sit side by side.
+template <int TT>
+struct KvSlots {
+  int64_t slot[TT];
+  uint32_t runs;                         // bit s: tokens 16 s .. 16 s + 15 are one aligned run
+};
+
+template <int TT>
+__device__ __forceinline__ void load_slots(const KvView& c, const int64_t* slots, int64_t t0,
+                                           int64_t tokens, KvSlots<TT>& sl) {
+  if (threadIdx.x < 64) {
+    const int i = (int)threadIdx.x;
+    const bool in = i < TT && t0 + i < tokens;
+    const int64_t s = in ? slots[t0 + i] : -1;
+    const uint32_t lo = __shfl((uint32_t)s, i & 48, 64), hi = __shfl((uint32_t)(s >> 32), i & 48, 64);
+    const int64_t head = (int64_t)((uint64_t)hi << 32 | lo);
+    const uint64_t ok = __ballot(slot_page(c, s) >= 0 && (head & 15) == 0 && s == head + (i & 15));
+    if (i < TT) sl.slot[i] = s;
+    if (i == 0) {
+      uint32_t runs = 0;
+#pragma unroll
+      for (int k = 0; k < TT / 16; k++)
+        if (((ok >> (16 * k)) & 0xFFFFu) == 0xFFFFu) runs |= 1u << k;
+      sl.runs = runs;
+    }
+  }
+  __syncthreads();
+}
+
+template <int MODE, int D, int TT>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvView c, const uint16_t* k, int64_t ks,
                                                             const uint16_t* v, int64_t vs,
                                                             const int64_t* slots, int64_t tokens) {
-  constexpr int G = kv_group<MODE>();
-  const int gph = c.dim / G, per = c.heads * gph;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= tokens * 2 * per) return;
-  const int64_t tok = i / (2 * per);
-  int r = (int)(i - tok * (2 * per));
-  const bool isv = r >= per;
-  if (isv) r -= per;
-  const int h = r / gph, g = r - h * gph;
-  const int64_t slot = slots[tok], page = slot_page(c, slot);
-  if (page < 0) return;
-  const int P = 1 << c.page_shift, at = (int)(slot & (P - 1));
-  const uint4* x = (const uint4*)(isv ? v + tok * vs : k + tok * ks) + (h * c.dim + g * G) / 8;
-  float y[G];
+  constexpr int G = kv_group<MODE>(), GPH = D / G, LD = TT + 4;
+  __shared__ KvSlots<TT> sl;
+  __shared__ __align__(16) uint8_t codes[D / 2 * LD], scales[GPH * LD];
+  const int h = (int)(blockIdx.x % (uint32_t)c.heads);
+  const int64_t t0 = (int64_t)(blockIdx.x / (uint32_t)c.heads) * TT;
+  load_slots<TT>(c, slots, t0, tokens, sl);
+  const int P = 1 << c.page_shift, live = (int)(tokens - t0 < TT ? tokens - t0 : TT);
+  const TensorScale kts = tensor_scale(MODE == 2 ? 0.0f : c.kam[h], MODE == 1);
+  const TensorScale vts = tensor_scale(MODE == 2 ? 0.0f : c.vam[h], MODE == 1);
+  // values first (the smaller half of the items), then keys
 #pragma unroll
-  for (int j = 0; j < G / 8; j++) unpack8(x[j], y + 8 * j);
-  uint32_t w[G / 8], scale;
-  if constexpr (MODE == 2) kv_quant32(y, w, scale);
-  else kv_quant16<MODE == 1>(y, tensor_scale((isv ? c.vam : c.kam)[h], MODE == 1), w[0], w[1], scale);
-  const int64_t ph = page * c.heads + h;
-  if (!isv) {
-    uint32_t* o = (uint32_t*)(c.kc + (ph * P + at) * (c.dim / 2) + g * (G / 2));
+  for (int it = (int)threadIdx.x; it < 2 * TT * GPH; it += kThreads) {
+    const bool isv = it < TT * GPH;
+    const int r = isv ? it : it - TT * GPH, tok = r / GPH, g = r % GPH;
+    if (tok >= live) continue;
+    const int64_t slot = sl.slot[tok], page = slot_page(c, slot);
+    if (page < 0) continue;
+    const uint4* x = (const uint4*)((isv ? v + (t0 + tok) * vs : k + (t0 + tok) * ks) + h * D + g * G);
+    float y[G];
 #pragma unroll
-    for (int j = 0; j < G / 8; j++) o[j] = w[j];
-    c.ks[(ph * P + at) * gph + g] = (uint8_t)scale;
-  } else {
-    uint8_t* o = c.vc + (ph * (c.dim / 2) + g * (G / 2)) * P + at;
+    for (int j = 0; j < G / 8; j++) unpack8(x[j], y + 8 * j);
+    uint32_t w[G / 8], scale;
+    if constexpr (MODE == 2) kv_quant32(y, w, scale);
+    else kv_quant16<MODE == 1>(y, isv ? vts : kts, w[0], w[1], scale);
+    if (isv) {
 #pragma unroll
-    for (int j = 0; j < G / 2; j++) o[(int64_t)j * P] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
-    c.vs[(ph * gph + g) * P + at] = (uint8_t)scale;
+      for (int j = 0; j < G / 2; j++)
+        codes[(g * (G / 2) + j) * LD + tok] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+      scales[g * LD + tok] = (uint8_t)scale;
+    } else {
+      const int64_t at = (page * c.heads + h) * P + (slot & (P - 1));
+      uint32_t* o = (uint32_t*)(c.kc + at * (D / 2) + g * (G / 2));
+      if constexpr (MODE == 2) *(uint4*)o = make_uint4(w[0], w[1], w[2], w[3]);
+      else *(uint2*)o = make_uint2(w[0], w[1]);
+      c.ks[at * GPH + g] = (uint8_t)scale;
+    }
+  }
+  __syncthreads();
+  for (int it = (int)threadIdx.x; it < (D / 2 + GPH) * (TT / 16); it += kThreads) {
+    const int seg = it % (TT / 16), row = it / (TT / 16);
+    const bool sc = row >= D / 2;
+    const uint8_t* from = (sc ? scales + (row - D / 2) * LD : codes + row * LD) + seg * 16;
+    // [page][head][row][P]
+    auto to = [&](int64_t slot, int64_t page) {
+      const int64_t ph = page * c.heads + h;
+      return (sc ? c.vs + (ph * GPH + row - D / 2) * P : c.vc + (ph * (D / 2) + row) * P) +
+             (slot & (P - 1));
+    };
+    if (sl.runs >> seg & 1) {
+      const uint32_t* f = (const uint32_t*)from;
+      const int64_t slot = sl.slot[seg * 16];
+      *(uint4*)to(slot, slot >> c.page_shift) = make_uint4(f[0], f[1], f[2], f[3]);
+    } else {
+      for (int e = 0; e < 16 && seg * 16 + e < live; e++) {
+        const int64_t slot = sl.slot[seg * 16 + e], page = slot_page(c, slot);
+        if (page >= 0) *to(slot, page) = from[e];
+      }
+    }
   }
 }
 
-// One lane per group, as above; slots without a page read as zeros.
+// Eight bf16 values of a code dword times its scale.
+__device__ __forceinline__ uint4 kv_decode8(uint32_t w, float s) {
+  const float2_t a = fp4x2_to_f32<0>(w, 1.0f), b = fp4x2_to_f32<1>(w, 1.0f);
+  const float2_t d = fp4x2_to_f32<2>(w, 1.0f), e = fp4x2_to_f32<3>(w, 1.0f);
+  return make_uint4(bf16x2_of(a.x * s, a.y * s), bf16x2_of(b.x * s, b.y * s),
+                    bf16x2_of(d.x * s, d.y * s), bf16x2_of(e.x * s, e.y * s));
+}
 template <int MODE>
+__device__ __forceinline__ float kv_scale(uint32_t code, float alpha) {
+  if constexpr (MODE == 2) return __builtin_ldexpf(1.0f, (int)code - 127);
+  else return alpha * e4m3_value(code & 0x7Fu);
+}
+
+// Slots without a page read as zeros.
+template <int MODE, int D, int TT>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvView c, const int64_t* slots,
                                                            int64_t tokens, uint16_t* k, int64_t ks,
                                                            uint16_t* v, int64_t vs) {
-  constexpr int G = kv_group<MODE>();
-  const int gph = c.dim / G, per = c.heads * gph;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= tokens * 2 * per) return;
-  const int64_t tok = i / (2 * per);
-  int r = (int)(i - tok * (2 * per));
-  const bool isv = r >= per;
-  if (isv) r -= per;
-  const int h = r / gph, g = r - h * gph;
-  const int64_t slot = slots[tok], page = slot_page(c, slot);
-  const int P = 1 << c.page_shift, at = (int)(slot & (P - 1));
-  uint32_t w[G / 8] = {};
-  float s = 0.0f;
-  if (page >= 0) {
-    const int64_t ph = page * c.heads + h;
-    uint32_t code;
-    if (!isv) {
-      const uint32_t* o = (const uint32_t*)(c.kc + (ph * P + at) * (c.dim / 2) + g * (G / 2));
+  constexpr int G = kv_group<MODE>(), GPH = D / G, LD = D / 2 + 1;
+  __shared__ KvSlots<TT> sl;
+  __shared__ uint32_t turned[TT * LD];   // [token][channel pair] bf16
+  const int h = (int)(blockIdx.x % (uint32_t)c.heads);
+  const int64_t t0 = (int64_t)(blockIdx.x / (uint32_t)c.heads) * TT;
+  load_slots<TT>(c, slots, t0, tokens, sl);
+  const int P = 1 << c.page_shift, live = (int)(tokens - t0 < TT ? tokens - t0 : TT);
+  const float ka = MODE == 2 ? 1.0f : tensor_scale(c.kam[h], MODE == 1).alpha;
+  const float va = MODE == 2 ? 1.0f : tensor_scale(c.vam[h], MODE == 1).alpha;
 #pragma unroll
-      for (int j = 0; j < G / 8; j++) w[j] = o[j];
-      code = c.ks[(ph * P + at) * gph + g];
+  for (int it = (int)threadIdx.x; it < D / 2 * (TT / 16); it += kThreads) {
+    const int seg = it % (TT / 16), row = it / (TT / 16), g = 2 * row / G;
+    uint32_t w[4] = {}, s[4] = {};
+    if (sl.runs >> seg & 1) {
+      const int64_t slot = sl.slot[seg * 16], ph = (slot >> c.page_shift) * c.heads + h;
+      const uint4 a = *(const uint4*)(c.vc + (ph * (D / 2) + row) * P + (slot & (P - 1)));
+      const uint4 b = *(const uint4*)(c.vs + (ph * GPH + g) * P + (slot & (P - 1)));
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
     } else {
-      const uint8_t* o = c.vc + (ph * (c.dim / 2) + g * (G / 2)) * P + at;
 #pragma unroll
-      for (int j = 0; j < G / 2; j++) w[j / 4] |= (uint32_t)o[(int64_t)j * P] << (8 * (j % 4));
-      code = c.vs[(ph * gph + g) * P + at];
+      for (int e = 0; e < 16; e++) {
+        const int64_t slot = sl.slot[seg * 16 + e], page = slot_page(c, slot);
+        if (page < 0) continue;
+        const int64_t ph = page * c.heads + h;
+        w[e / 4] |= (uint32_t)c.vc[(ph * (D / 2) + row) * P + (slot & (P - 1))] << (8 * (e % 4));
+        s[e / 4] |= (uint32_t)c.vs[(ph * GPH + g) * P + (slot & (P - 1))] << (8 * (e % 4));
+      }
     }
-    if constexpr (MODE == 2) s = __builtin_ldexpf(1.0f, (int)code - 127);
-    else s = tensor_scale((isv ? c.vam : c.kam)[h], MODE == 1).alpha * e4m3_value(code & 0x7Fu);
+    static_for<16>([&](auto ee) {
+      constexpr int e = decltype(ee)::value;
+      const float2_t x = fp4x2_to_f32<e % 4>(w[e / 4], 1.0f);
+      const float f = kv_scale<MODE>((s[e / 4] >> (8 * (e % 4))) & 255u, va);
+      turned[(seg * 16 + e) * LD + row] = bf16x2_of(x.x * f, x.y * f);
+    });
   }
-  uint4* o = (uint4*)(isv ? v + tok * vs : k + tok * ks) + (h * c.dim + g * G) / 8;
 #pragma unroll
-  for (int j = 0; j < G / 8; j++) {
-    float y[8];
-    const float2_t a = fp4x2_to_f32<0>(w[j], 1.0f), b = fp4x2_to_f32<1>(w[j], 1.0f);
-    const float2_t d = fp4x2_to_f32<2>(w[j], 1.0f), e = fp4x2_to_f32<3>(w[j], 1.0f);
-    y[0] = a.x * s; y[1] = a.y * s; y[2] = b.x * s; y[3] = b.y * s;
-    y[4] = d.x * s; y[5] = d.y * s; y[6] = e.x * s; y[7] = e.y * s;
-    o[j] = pack8(y);
+  for (int it = (int)threadIdx.x; it < TT * (D / 8); it += kThreads) {
+    const int tok = it / (D / 8), ch = it % (D / 8) * 8;
+    if (tok >= live) continue;
+    const int64_t slot = sl.slot[tok], page = slot_page(c, slot);
+    uint32_t w = 0, s = 0;
+    if (page >= 0) {
+      const int64_t at = (page * c.heads + h) * P + (slot & (P - 1));
+      w = *(const uint32_t*)(c.kc + at * (D / 2) + ch / 2);
+      s = c.ks[at * GPH + ch / G];
+    }
+    *(uint4*)(k + (t0 + tok) * ks + h * D + ch) = kv_decode8(w, kv_scale<MODE>(s, ka));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = (int)threadIdx.x; it < TT * (D / 8); it += kThreads) {
+    const int tok = it / (D / 8), ch = it % (D / 8) * 8;
+    if (tok >= live) continue;
+    const uint32_t* f = turned + tok * LD + ch / 2;
+    *(uint4*)(v + (t0 + tok) * vs + h * D + ch) = make_uint4(f[0], f[1], f[2], f[3]);
   }
 }
 

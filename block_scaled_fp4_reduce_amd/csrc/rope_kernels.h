@@ -242,20 +242,32 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
 }
 
 // dw = sum of the workgroups' partials, in a fixed order and 64 bits (the
-// sum runs over every token): 16 columns per workgroup, 16 rows at a time.
-__global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_dw_kernel(const float* partial,
-                                                                       int rows, int dim, float* dqw,
-                                                                       float* dkw) {
-  __shared__ double red[16][16];
-  const int c = (int)threadIdx.x & 15, r = (int)threadIdx.x >> 4;
-  const int j = (int)blockIdx.x * 16 + c;
+// sum runs over every token): 8 columns per workgroup, 128 rows at a time, so
+// that a thread's few loads are all on their way at once.
+constexpr int kDwThreads = 1024, kDwCols = 8, kDwRows = kDwThreads / kDwCols;
+__global__ __launch_bounds__(kDwThreads) void qk_norm_rope_dw_kernel(const float* partial, int rows,
+                                                                     int dim, float* dqw,
+                                                                     float* dkw) {
+  __shared__ double red[kDwRows][kDwCols];
+  const int c = (int)threadIdx.x % kDwCols, r = (int)threadIdx.x / kDwCols;
+  const int j = (int)blockIdx.x * kDwCols + c;
   double t = 0.0;
-  if (j < 2 * dim)
-    for (int i = r; i < rows; i += 16) t += (double)partial[(int64_t)i * 2 * dim + j];
+  if (j < 2 * dim) {
+    float x[kRopeMaxGroups / kDwRows];
+#pragma unroll
+    for (int i = 0; i < kRopeMaxGroups / kDwRows; i++) {
+      const int row = r + i * kDwRows;
+      x[i] = row < rows ? partial[(int64_t)row * 2 * dim + j] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeMaxGroups / kDwRows; i++) t += (double)x[i];
+  }
   red[r][c] = t;
-  __syncthreads();
+  for (int half = kDwRows / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (r < half) red[r][c] = t += red[r + half][c];
+  }
   if (r == 0 && j < 2 * dim) {
-    for (int i = 1; i < 16; i++) t += red[i][c];
     float* out = j < dim ? dqw : dkw;
     if (out) out[j < dim ? j : j - dim] = (float)t;
   }
