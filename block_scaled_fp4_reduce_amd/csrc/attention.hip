@@ -115,6 +115,8 @@ int64_t rope_bwd_groups(const fp4_qk_rope* a, const RopeArgs& r) {
 }
 
 // ------------------------------------------------------------------ attention
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;   // query rows: the kernels count them in 32 bits
+
 int check_attention_sizes(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   if (!x) return FP4_E_NULL;
   if (int rc = check_kv_cache(c)) return rc;
@@ -123,6 +125,7 @@ int check_attention_sizes(const fp4_kv_cache* c, const fp4_kv_queries* x) {
       x->table_width > (((int64_t)1 << 31) - 1) / c->page_size)
     return FP4_E_SHAPE;
   if (x->q_heads < 1 || x->q_heads > 65536 || x->q_heads % c->heads) return FP4_E_SHAPE;
+  if (x->tokens > kMaxRows / x->q_heads || x->seqs > kMaxRows / x->q_heads) return FP4_E_SHAPE;
   if (!x->cu_q && x->tokens != x->seqs) return FP4_E_SHAPE;
   if (x->window < 0 || !(x->softcap >= 0.0f) || std::isinf(x->softcap) || !std::isfinite(x->scale))
     return FP4_E_SHAPE;
@@ -148,7 +151,7 @@ int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16
 // context.
 struct AttnPlan {
   int nt;
-  int64_t tiles, splits;
+  int64_t tiles, splits, want, places;
 };
 
 AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
@@ -163,37 +166,49 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   int64_t keys = x->table_width * c->page_size;
   if (x->window > 0 && keys > x->window + most) keys = x->window + most;
   const int64_t blocks = cdiv(keys, kAttnKeys);
-  const int64_t want = cdiv(num_cus() * (p.nt ? 4 : 2), p.tiles * c->heads);
-  const int64_t room = cdiv(blocks, 4);
-  p.splits = want < room ? want : room;
+  // Workgroups wanted per kv head.  How they are shared out among the
+  // sequences depends on lengths that only the device knows (item_of); a
+  // tile gets at most four times an even share.
+  const int per_cu = p.nt == 0 ? 4 : (p.nt == 2 || c->head_dim == 256 ? 2 : 3);
+  p.want = cdiv(per_cu * (int64_t)num_cus(), c->heads);
+  const int64_t share = cdiv(4 * p.want, p.tiles), room = cdiv(blocks, 4);
+  p.splits = p.tiles >= p.want ? 1 : (share < room ? share : room);
   p.splits = p.splits < 1 ? 1 : (p.splits > 64 ? 64 : p.splits);
+  // every tile has one part and the rest come to a.want together
+  p.places = p.tiles + (p.splits > 1 ? p.want : 0);
   return p;
 }
 
 size_t attention_ws(const fp4_kv_cache* c, const fp4_kv_queries* x, const AttnPlan& p) {
   if (p.splits <= 1) return 0;
-  return (size_t)p.splits * x->tokens * x->q_heads * (c->head_dim + 2) * sizeof(float);
+  return (size_t)p.splits * x->tokens * x->q_heads * (c->head_dim + 2) * sizeof(float) +
+         (size_t)x->tokens * x->q_heads * sizeof(int);
 }
 
 template <int MODE, int D>
 hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(p.tiles * p.splits * a.c.heads);
+  const unsigned grid = (unsigned)(p.places * a.c.heads);
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
-    e = launch(kv_tiled_kernel<MODE, D>, grid, kThreads, st, a, (uint32_t)p.tiles);
-  } else if (p.nt == 1) {
-    e = launch(kv_attention_kernel<MODE, D, 1, 4>, grid, 256, st, a);
+    e = launch(kv_tiled_kernel<MODE, D>, grid, kThreads, st, a);
   } else {
-    if constexpr (D < 256) e = launch(kv_attention_kernel<MODE, D, 2, 4>, grid, 256, st, a);
+    const bool wide = a.c.page_shift >= 6;
+    auto go = [&](auto nt) {
+      constexpr int N = decltype(nt)::value;
+      return wide ? launch(kv_attention_kernel<MODE, D, N, 4, true>, grid, 256, st, a)
+                  : launch(kv_attention_kernel<MODE, D, N, 4, false>, grid, 256, st, a);
+    };
+    if (p.nt == 1) e = go(std::integral_constant<int, 1>{});
+    else if constexpr (D < 256) e = go(std::integral_constant<int, 2>{});
   }
   if (p.splits > 1) {
-    // as many lanes on a row's parts as keep a lane at 4 of them
+    // as many lanes on a row's parts as leave a lane 4 of them
     const int lanes = D / 4, most = kThreads / lanes;
-    int parts = 1;
-    while (parts < most && parts * 4 < p.splits) parts *= 2;
+    int groups = 1;
+    while (groups < most && groups * 4 < p.splits) groups *= 2;
     e = first(e, launch(kv_attention_join_kernel<MODE, D>,
-                        (unsigned)cdiv(a.tokens * a.hq, kThreads / (lanes * parts)), kThreads, st,
-                        a, parts));
+                        (unsigned)cdiv(a.tokens * a.hq, kThreads / (lanes * groups)), kThreads, st,
+                        a, groups));
   }
   return e;
 }
@@ -271,7 +286,7 @@ int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* o
   if (!aligned(ws, 16)) return FP4_E_ALIGN;
   if (x->tokens == 0) return FP4_OK;
   const AttnPlan p = attention_plan(c, x);
-  if (p.tiles > (((int64_t)1 << 32) - 1) / kThreads / p.splits / c->heads) return FP4_E_SHAPE;
+  if (p.places > (((int64_t)1 << 32) - 1) / kThreads / c->heads) return FP4_E_SHAPE;
   const size_t need = attention_ws(c, x, p);
   if (need > 0 && !ws) return FP4_E_NULL;
   if (ws_bytes < need) return FP4_E_WORKSPACE;
@@ -294,8 +309,11 @@ int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* o
   a.scale = x->scale;
   a.cap = x->softcap;
   a.splits = (int)p.splits;
+  a.want = (uint32_t)p.want;
   a.po = (float*)ws;
-  a.pm = a.po + (need ? p.splits * x->tokens * x->q_heads * c->head_dim : 0);
+  const int64_t rows = need ? x->tokens * x->q_heads : 0;
+  a.pm = a.po + p.splits * rows * c->head_dim;
+  a.parts = (int*)(a.pm + p.splits * rows * 2);
   hipStream_t st = (hipStream_t)stream;
   switch (kv_mode(c)) {
     case 0: return launched(launch_attention<0>(c->head_dim, p, a, st));

@@ -38,9 +38,11 @@ struct AttnArgs {
   uint16_t* out;
   float* lse;                            // [tokens][hq] or NULL
   float *po, *pm;                        // partials [splits][tokens][hq][D], [..][2] (max, sum)
+  int* parts;                            // [tokens][hq] parts in use
   int64_t qs, os;                        // elements between tokens
   int64_t tokens, seqs, width;
   int hq, group, window, splits;
+  uint32_t want;                         // workgroups wanted per kv head
   float scale, cap;                      // cap 0: none
 };
 
@@ -102,56 +104,176 @@ __device__ __forceinline__ float col_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// A tile of query rows: rows row0 .. row0 + M - 1 of sequence b, row r being
-// token r / group with head r % group of the kv head's own.
-struct RowTile {
-  int64_t b, tok0;                       // the sequence's first token
-  int64_t row0, rows;                    // rows of the whole sequence
-  int64_t len, n;
+// A workgroup's work: rows row0 .. row0 + M - 1 of sequence b, row r being
+// token r / group with head r % group of the kv head's own, and part `split`
+// of the `parts` that their context is cut into.  All rows together stay
+// below 2^31.
+struct Work {
+  uint32_t b, tok0;                      // the sequence's first token
+  uint32_t row0, rows;                   // rows of the whole sequence
+  int len, n;                            // cached tokens, new ones
+  uint32_t split, parts;
 };
 
-__device__ __forceinline__ int64_t cu_at(const AttnArgs& a, int64_t b) {
-  const int64_t v = a.cu[b];
-  return v < 0 ? 0 : (v > a.tokens ? a.tokens : v);
+__device__ __forceinline__ uint32_t cu_at(const AttnArgs& a, uint32_t b) {
+  const int v = a.cu[b];
+  return v < 0 ? 0 : (v > (int)a.tokens ? (uint32_t)a.tokens : (uint32_t)v);
 }
 
-// Tile `t` of the grid.  Sequence b's tiles start at floor(cu[b] group / M) + b,
-// which leaves room for every sequence's ceil(n group / M) whatever the n, so
-// the grid needs no sizes from the device; ids between have no rows.  The
-// search takes 64 boundaries at a time, one a lane.
-__device__ __forceinline__ bool row_tile(const AttnArgs& a, int64_t t, int M, RowTile& r) {
-  int64_t first = t;
-  if (a.cu) {
-    int64_t lo = 0, n = a.seqs;          // the answer is in [lo, lo + n)
-    while (n > 1) {
-      const int64_t step = (n + 63) / 64;
-      const int64_t at = lo + step * (int64_t)(threadIdx.x & 63);
-      const bool below = at < lo + n && cu_at(a, at) * a.group / M + at <= t;
-      const int64_t k = __popcll(__ballot(below)) - 1;   // monotone: a prefix of the lanes
-      const int64_t end = lo + n;
-      lo += step * (k < 0 ? 0 : k);
-      n = end - lo < step ? end - lo : step;
-    }
-    r.b = lo;
-    r.tok0 = cu_at(a, lo);
-    const int64_t next = cu_at(a, lo + 1);
-    r.n = next > r.tok0 ? next - r.tok0 : 0;
-    first = r.tok0 * a.group / M + lo;
-  } else {
-    const int64_t per = (a.group + M - 1) / M;
-    r.b = t / per;
-    first = r.b * per;
-    if (r.b >= a.seqs) return false;
-    r.tok0 = r.b;
-    r.n = 1;
+// Without parts, tile `t` of the grid: sequence b's tiles start at
+// floor(cu[b] group / M) + b, which leaves room for every sequence's
+// ceil(n group / M) whatever the n, so the grid needs no sizes from the
+// device; ids between have no rows.  The search takes 64 boundaries at a
+// time, one a lane.  Returns the tile of the sequence.
+template <uint32_t M>
+__device__ __forceinline__ uint32_t tile_of(const AttnArgs& a, uint32_t t, Work& w) {
+  const uint32_t group = (uint32_t)a.group;
+  if (!a.cu) {
+    const uint32_t per = (group + M - 1) / M;
+    w.b = t / per;
+    return t - w.b * per;
   }
-  r.rows = r.n * a.group;
-  r.row0 = (t - first) * M;
-  if (r.row0 < 0 || r.row0 >= r.rows) return false;
-  r.len = a.lens[r.b];
+  uint32_t lo = 0, n = (uint32_t)a.seqs;             // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const uint32_t step = (n + 63) / 64;
+    const uint32_t at = step * (threadIdx.x & 63);
+    const bool below = at < n && cu_at(a, lo + at) * group / M + lo + at <= t;
+    const int k = __popcll(__ballot(below)) - 1;     // monotone: a prefix of the lanes
+    const uint32_t skip = step * (uint32_t)(k < 0 ? 0 : k);
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  w.b = __builtin_amdgcn_readfirstlane(lo);
+  return t - (cu_at(a, w.b) * group / M + w.b);      // wraps to no tile before the first
+}
+
+// Blocks of 64 keys that `n` new tokens at the end of `len` can reach.
+__device__ __forceinline__ uint32_t blocks_in_reach(const AttnArgs& a, int64_t len, int64_t n) {
   const int64_t most = a.width << a.c.page_shift;
-  if (r.len > most) r.len = most;
+  int64_t reach = len > most ? most : len;
+  if (a.window > 0 && reach > a.window + n) reach = a.window + n;
+  return reach > 0 ? (uint32_t)((reach + kAttnKeys - 1) / kAttnKeys) : 0;
+}
+
+// Running sum over the wave by DPP: within rows of 16, then across.
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T dpp_add(T v) {
+  return v + __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               ROWS, 0xF, false));
+}
+template <typename T>
+__device__ __forceinline__ T wave_prefix(T v) {      // inclusive
+  v = dpp_add<0x111, 0xF>(v);            // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);            // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);         // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// With parts, item `t` of the list of (sequence, tile, part) in that order.  A
+// sequence's context is cut into its share of a.want by blocks among the
+// tiles of all sequences, so that every workgroup gets about the same number
+// whatever the mixture of lengths (only the device knows them), but into at
+// most a.splits parts of at least 4 blocks.  The list has no holes: hardware
+// deals workgroups out to its engines in turn, and ids that ended at once at a
+// fixed stride left whole engines idle (a prompt's 700 us became 2.8 ms).
+template <uint32_t M>
+__device__ __forceinline__ uint32_t item_of(const AttnArgs& a, uint32_t t, Work& w) {
+  const uint32_t lane = threadIdx.x & 63, seqs = (uint32_t)a.seqs;
+  uint32_t c0 = 0, n = 0, tiles = 0, blocks = 0;
+  int len = 0;
+  auto size = [&](uint32_t first) {      // sequence first + lane
+    const uint32_t b = first + lane;
+    const bool in = b < seqs;
+    const uint32_t bb = in ? b : 0;
+    len = a.lens[bb];
+    c0 = b;
+    n = in ? 1 : 0;
+    if (a.cu) {
+      c0 = cu_at(a, bb);
+      const uint32_t c1 = cu_at(a, bb + 1);
+      n = in && c1 > c0 ? c1 - c0 : 0;
+    }
+    tiles = (n * (uint32_t)a.group + M - 1) / M;
+    blocks = blocks_in_reach(a, len, n);
+  };
+  float total = 0.0f;                    // tiles x blocks
+  for (uint32_t first = 0; first < seqs; first += 64) {
+    size(first);
+    total += __uint_as_float(lane_value(__float_as_uint(wave_prefix((float)tiles * (float)blocks)), 63));
+  }
+  const float each = total > 0.0f ? (float)a.want / total : 0.0f;
+  uint32_t before = 0;                   // items of the sequences before `first`
+  for (uint32_t first = 0; first < seqs; first += 64) {
+    if (seqs > 64) size(first);
+    const uint32_t most = min((blocks + 3) / 4, (uint32_t)a.splits);
+    const uint32_t parts = max(1u, min(most, (uint32_t)__builtin_rintf((float)blocks * each)));
+    const uint32_t items = tiles * parts, upto = wave_prefix(items);
+    const uint64_t past = __ballot(before + upto > t);
+    if (past) {
+      const int k = __builtin_ctzll(past);
+      w.b = first + k;
+      w.parts = lane_value(parts, k);
+      w.tok0 = lane_value(c0, k);
+      w.n = (int)lane_value(n, k);
+      w.len = (int)lane_value((uint32_t)len, k);
+      const uint32_t at = t - before - (lane_value(upto, k) - lane_value(items, k));
+      const uint32_t tile = at / w.parts;
+      w.split = at - tile * w.parts;
+      return tile;
+    }
+    before += lane_value(upto, 63);
+  }
+  return ~0u;
+}
+
+// The work of place `t` for one head; false where there is none.
+template <uint32_t M>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, uint32_t t, Work& w) {
+  uint32_t tile;
+  if (a.splits > 1) {
+    tile = item_of<M>(a, t, w);
+    if (tile == ~0u) return false;
+  } else {
+    w.split = 0;
+    w.parts = 1;
+    tile = tile_of<M>(a, t, w);
+    if (w.b >= (uint32_t)a.seqs) return false;
+    w.tok0 = w.b;
+    w.n = 1;
+    if (a.cu) {
+      w.tok0 = cu_at(a, w.b);
+      const uint32_t next = cu_at(a, w.b + 1);
+      w.n = next > w.tok0 ? (int)(next - w.tok0) : 0;
+    }
+    w.len = a.lens[w.b];
+  }
+  w.rows = (uint32_t)w.n * (uint32_t)a.group;
+  if ((uint64_t)tile * M >= w.rows) return false;
+  w.row0 = tile * M;
+  const int64_t most = a.width << a.c.page_shift;    // below 2^31
+  if (w.len > most) w.len = (int)most;
   return true;
+}
+
+// Partial sums: [split][token][head], and how many parts a row has.
+__device__ __forceinline__ int64_t row_at(const AttnArgs& a, const Work& w, int h, uint32_t row) {
+  const uint32_t tok = row / (uint32_t)a.group;
+  return (int64_t)(w.tok0 + tok) * a.hq + h * a.group + (row - tok * (uint32_t)a.group);
+}
+// Notes the parts of `count` rows; a part without blocks is an empty sum.
+__device__ __forceinline__ void note_parts(const AttnArgs& a, const Work& w, int h, uint32_t count,
+                                           bool empty, uint32_t threads) {
+  for (uint32_t r = threadIdx.x; r < count && w.row0 + r < w.rows; r += threads) {
+    const int64_t at = row_at(a, w, h, w.row0 + r);
+    if (w.split == 0) a.parts[at] = (int)w.parts;
+    if (empty) *(float2*)(a.pm + (w.split * a.tokens * a.hq + at) * 2) =
+        make_float2(-__builtin_inff(), 0.0f);
+  }
 }
 
 // One wave's share of 64 cached tokens: lane (c = lane & 15, g = lane >> 4)
@@ -160,71 +282,114 @@ __device__ __forceinline__ bool row_tile(const AttnArgs& a, int64_t t, int M, Ro
 // pairs 16 T + c.  The row order of the keys is what makes a lane's weights
 // of the first product those of 16 consecutive tokens.
 template <int MODE, int D>
-struct KvFragment {
+struct KeyFragment {
   static constexpr int G = MODE == 2 ? 32 : 16;
-  static constexpr int KD = D / 32;                  // dwords of a key; pieces of the values
-  uint32_t k[4][KD], ks[4];
-  u32x4_t v[KD], vs[KD];
+  uint32_t k[4][D / 32], s[4];
+};
+template <int MODE, int D>
+struct ValueFragment {
+  u32x4_t v[D / 32], s[D / 32];
 };
 
+// Page ids of a lane's keys and values, -1 outside the cache or the table.
 struct KvPages {
-  int k, v;                              // page ids, -1 outside the cache or the table
+  int k, v;
 };
 
-__device__ __forceinline__ int page_id(const AttnArgs& a, int64_t b, int64_t key) {
+__device__ __forceinline__ int page_id(const AttnArgs& a, uint32_t b, int64_t key) {
   const int64_t i = key >> a.c.page_shift;
   if (i >= a.width) return -1;
   const int p = a.pt[b * a.width + i];
   return p >= 0 && p < a.c.pages ? p : -1;
 }
 
-__device__ __forceinline__ KvPages load_pages(const AttnArgs& a, int64_t b, int64_t base) {
+// With pages of 64 tokens and more a block lies in one page, whose address is
+// the same for the whole wave (scalar arithmetic); with smaller ones each
+// lane follows its own.
+template <bool WIDE>
+__device__ __forceinline__ KvPages load_pages(const AttnArgs& a, uint32_t b, int64_t base) {
   const int lane = (int)threadIdx.x & 63;
   KvPages p;
-  p.k = page_id(a, b, base + 16 * ((lane & 15) >> 2));
-  p.v = page_id(a, b, base + 16 * (lane >> 4));
+  if constexpr (WIDE) {
+    p.k = p.v = page_id(a, b, base);
+  } else {
+    p.k = page_id(a, b, base + 16 * ((lane & 15) >> 2));
+    p.v = page_id(a, b, base + 16 * (lane >> 4));
+  }
   return p;
 }
 
-template <int MODE, int D>
-__device__ __forceinline__ void load_kv(const AttnArgs& a, int h, int64_t base, KvPages pg,
-                                        KvFragment<MODE, D>& f) {
-  constexpr int G = KvFragment<MODE, D>::G, KD = D / 32;
+// N bytes at `base` + `lane` + `step`, the first (and the step) the same for
+// the whole wave if WIDE: then through a buffer resource, whose base and
+// offset are scalars, so that a block's addresses cost no vector arithmetic.
+template <int N, bool WIDE>
+struct KvLoad {
+  typedef uint32_t T __attribute__((ext_vector_type(N >= 4 ? N / 4 : 1)));
+  static __device__ __forceinline__ T at(const uint8_t* base, uint32_t lane, uint32_t step) {
+    T v;
+    if constexpr (WIDE) {
+      // a page's part of one head is under 2^31 bytes (page_size * head_dim / 2 <= 2^19)
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0x7FFFFFF0,
+                                                       0x00020000);
+      if constexpr (N == 16) v = __builtin_amdgcn_raw_buffer_load_b128(r, lane, step, 0);
+      else if constexpr (N == 8) v = __builtin_amdgcn_raw_buffer_load_b64(r, lane, step, 0);
+      else if constexpr (N == 4) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, lane, step, 0);
+      else if constexpr (N == 2) v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, lane, step, 0);
+      else v[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, lane, step, 0);
+    } else {
+      const uint8_t* p = base + lane + step;
+      if constexpr (N >= 4) v = *(const T*)p;
+      else if constexpr (N == 2) v[0] = *(const uint16_t*)p;
+      else v[0] = *p;
+    }
+    return v;
+  }
+};
+
+template <int MODE, int D, bool WIDE>
+__device__ __forceinline__ void load_keys(const AttnArgs& a, int h, int64_t base, KvPages pg,
+                                          KeyFragment<MODE, D>& f) {
+  constexpr int G = KeyFragment<MODE, D>::G, KD = D / 32;
   const int lane = (int)threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int P = 1 << a.c.page_shift;
+  const int P = 1 << a.c.page_shift, seg = 16 * (c >> 2);
   const int64_t pk = (int64_t)(pg.k < 0 ? 0 : pg.k) * a.c.heads + h;
-  const int64_t pv = (int64_t)(pg.v < 0 ? 0 : pg.v) * a.c.heads + h;
-  const int ak = (int)((base + 16 * (c >> 2)) & (P - 1)) + (c & 3);
-  const int av = (int)((base + 16 * g) & (P - 1));
-  const uint8_t* kc = a.c.kc + (pk * P + ak) * (D / 2) + g * (D / 8);
+  // token of the page (the same for the wave when WIDE), and the lane's offset from it
+  const int64_t at = pk * P + (int)((WIDE ? base : base + seg) & (P - 1));
+  const uint32_t row = (WIDE ? seg : 0) + (c & 3);
+  const uint8_t* kc = a.c.kc + at * (D / 2);
+  const uint8_t* ks = a.c.ks + at * (D / G);
+  const uint32_t ko = row * (D / 2) + g * (D / 8), so = row * (D / G) + g * (D / 4) / G;
+  constexpr int KB = KD * 4 > 16 ? 16 : KD * 4;      // bytes of a load
   constexpr int SB = D / 4 >= G ? D / 4 / G : 1;     // scale bytes of a lane's channels
-  const uint8_t* ks = a.c.ks + (pk * P + ak) * (D / G) + g * (D / 4) / G;
 #pragma unroll
   for (int t = 0; t < 4; t++) {
-    if constexpr (KD == 2) {
-      const u32x2_t w = *(const u32x2_t*)(kc + t * 4 * (D / 2));
-      f.k[t][0] = w[0];
-      f.k[t][1] = w[1];
-    } else {
 #pragma unroll
-      for (int i = 0; i < KD; i += 4) {
-        const u32x4_t w = *(const u32x4_t*)(kc + t * 4 * (D / 2) + i * 4);
+    for (int i = 0; i < KD; i += KB / 4) {
+      const auto w = KvLoad<KB, WIDE>::at(kc, ko + (t * 4 * (D / 2) + i * 4), 0);
 #pragma unroll
-        for (int e = 0; e < 4; e++) f.k[t][i + e] = w[e];
-      }
+      for (int e = 0; e < KB / 4; e++) f.k[t][i + e] = w[e];
     }
-    const uint8_t* s = ks + t * 4 * (D / G);
-    if constexpr (SB == 4) f.ks[t] = *(const uint32_t*)s;
-    else if constexpr (SB == 2) f.ks[t] = *(const uint16_t*)s;
-    else f.ks[t] = *s;
+    f.s[t] = KvLoad<SB, WIDE>::at(ks, so + t * 4 * (D / G), 0)[0];
   }
-  const uint8_t* vc = a.c.vc + (pv * (D / 2) + c) * P + av;
-  const uint8_t* vs = a.c.vs + pv * (D / G) * P + av;
+}
+
+template <int MODE, int D, bool WIDE>
+__device__ __forceinline__ void load_values(const AttnArgs& a, int h, int64_t base, KvPages pg,
+                                            ValueFragment<MODE, D>& f) {
+  constexpr int G = KeyFragment<MODE, D>::G, KD = D / 32;
+  const int lane = (int)threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int P = 1 << a.c.page_shift;
+  const int64_t pv = (int64_t)(pg.v < 0 ? 0 : pg.v) * a.c.heads + h;
+  const int at = (int)((WIDE ? base : base + 16 * g) & (P - 1));
+  const uint32_t tok = WIDE ? 16 * g : 0;
+  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + at;
+  const uint8_t* vs = a.c.vs + pv * (D / G) * P + at;
+  const uint32_t vo = ((uint32_t)c << a.c.page_shift) + tok;
+  const uint32_t so = ((uint32_t)(MODE == 2 ? 0 : c >> 3) << a.c.page_shift) + tok;
 #pragma unroll
   for (int T = 0; T < KD; T++) {
-    f.v[T] = *(const u32x4_t*)(vc + (int64_t)T * 16 * P);
-    const int sg = MODE == 2 ? T : 2 * T + (c >> 3);
-    f.vs[T] = *(const u32x4_t*)(vs + (int64_t)sg * P);
+    f.v[T] = KvLoad<16, WIDE>::at(vc, vo, (uint32_t)(16 * T) << a.c.page_shift);
+    f.s[T] = KvLoad<16, WIDE>::at(vs, so, (uint32_t)(MODE == 2 ? T : 2 * T) << a.c.page_shift);
   }
 }
 
@@ -287,46 +452,40 @@ __device__ __forceinline__ void value_operands(uint32_t w0, uint32_t w1, uint32_
   }
 }
 
-// Queries of one column as B operands: step s, slot j is channel D/4 g + 8 s + j.
+// Queries of one column as B operands of NS steps, each lane's 8 channels of
+// step s at q + s * STRIDE; `reduce` takes a maximum over the column's lanes.
 // Returns the factor that turns the products into scores in powers of two.
-template <int MODE, int D>
-__device__ __forceinline__ float load_query(const AttnArgs& a, int h, const uint16_t* q, bool live,
-                                            u32x4_t (&o)[D / 32]) {
-  const int g = ((int)threadIdx.x & 63) >> 4;
+// A scale of 0 makes every score 0; a negative one goes to the queries, so
+// that the factor is positive.
+template <int MODE, int NS, int STRIDE, typename R>
+__device__ __forceinline__ float load_query(const AttnArgs& a, int h, const uint16_t* q,
+                                            u32x4_t (&o)[NS], R&& reduce) {
   const float k = fabsf(a.scale) * kLog2e;
-  if (a.scale == 0.0f) live = false;                 // every score is 0
-  float y[D / 4];
+  const uint32_t keep = a.scale == 0.0f ? 0u : ~0u, flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-  for (int s = 0; s < D / 32; s++) {
-    const uint4 w = live ? *(const uint4*)(q + g * (D / 4) + s * 8) : make_uint4(0, 0, 0, 0);
-    unpack8(w, y + 8 * s);
-  }
-  if (a.scale < 0.0f) {
+  for (int s = 0; s < NS; s++) o[s] = *(const u32x4_t*)(q + s * STRIDE);
+  if (keep == 0 || flip) {
 #pragma unroll
-    for (int i = 0; i < D / 4; i++) y[i] = -y[i];
+    for (int s = 0; s < NS; s++) o[s] = (o[s] & keep) ^ flip;
   }
   if constexpr (MODE == 2) {
-#pragma unroll
-    for (int s = 0; s < D / 32; s++) {
-      const uint4 w = pack8(y + 8 * s);
-      o[s] = u32x4_t{w.x, w.y, w.z, w.w};
-    }
     return fmaxf(k, 0x1p-126f);
   } else {
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < D / 4; i++) m = fmaxf(m, fabsf(y[i]));
-    m = col_max(m);
-    int shift = 141 - (int)(__float_as_uint(m) >> 23);           // 2^14 <= m 2^shift < 2^15
+    for (int s = 0; s < NS; s++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        m = max(m, max(o[s][i] & 0x7FFFu, (o[s][i] >> 16) & 0x7FFFu));
+    const float top = reduce(__uint_as_float(m << 16));
+    int shift = 141 - (int)(__float_as_uint(top) >> 23);         // 2^14 <= top 2^shift < 2^15
     shift = shift > 127 ? 127 : shift;
 #pragma unroll
-    for (int s = 0; s < D / 32; s++)
+    for (int s = 0; s < NS; s++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float x0 = __builtin_ldexpf(y[8 * s + 2 * i], shift);
-        const float x1 = __builtin_ldexpf(y[8 * s + 2 * i + 1], shift);
-        o[s][i] = bits_of(f16x2_t{(_Float16)x0, (_Float16)x1});
-      }
+      for (int i = 0; i < 4; i++)
+        o[s][i] = bits_of(f16x2_t{(_Float16)__builtin_ldexpf(bf16_lo(o[s][i]), shift),
+                                  (_Float16)__builtin_ldexpf(bf16_hi(o[s][i]), shift)});
     const float alpha = a.c.kam[h] / (6.0f * (MODE == 1 ? 256.0f : 448.0f));
     return fmaxf(__builtin_ldexpf(k * alpha, -shift), 0x1p-126f);
   }
@@ -340,74 +499,114 @@ __device__ __forceinline__ float capped(float s, float in, float out) {
 
 // NT columns of 16 query rows, WAVES waves that take the blocks of 64 keys of
 // the workgroup's part of the context in turn and join their sums at the end.
-template <int MODE, int D, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_attention_kernel(AttnArgs a) {
+template <int MODE, int D, int NT, int WAVES, bool WIDE>
+__global__ __launch_bounds__(64 * WAVES, D == 256 || NT == 2 ? 2 : (D == 128 ? 3 : 4))
+void kv_attention_kernel(AttnArgs a) {
   constexpr int KD = D / 32, M = 16 * NT;
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f;   // weights carry 2^kOff
+  // the running maximum may lag by 2^kLag before everything is rescaled (fp16
+  // weights then stay under 2^15; bf16 and the sums have room)
+  constexpr float kLag = MODE == 2 ? 8.0f : 3.0f;
   __shared__ float so[WAVES][16][D + 4];
   __shared__ float sm[WAVES][16][2];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  __shared__ u32x4_t sq[NT][KD][64];     // the queries, each lane's operand (registers are short)
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  uint32_t id = blockIdx.x;
-  const int h = (int)(id % (uint32_t)a.c.heads);
-  id /= (uint32_t)a.c.heads;
-  const int split = (int)(id % (uint32_t)a.splits);
-  RowTile rt;
-  if (!row_tile(a, id / (uint32_t)a.splits, M, rt)) return;
+  // heads fastest: consecutive ids go to consecutive XCDs
+  const uint32_t place = blockIdx.x / (uint32_t)a.c.heads;
+  const int h = (int)(blockIdx.x - place * (uint32_t)a.c.heads);
+  Work rt;
+  if (!find_work<M>(a, place, rt)) return;
+  const int split = (int)rt.split;
   // reach of the tile's rows: [lo, hi) of each column, and of all together
-  const int64_t last = rt.row0 + M < rt.rows ? rt.row0 + M - 1 : rt.rows - 1;
-  auto hi_of = [&](int64_t row) {
-    const int64_t x = rt.len - rt.n + row / a.group + 1;
+  const uint32_t group = (uint32_t)a.group;
+  const uint32_t last = rt.rows - rt.row0 > M ? rt.row0 + M - 1 : rt.rows - 1;
+  auto hi_of = [&](uint32_t row) {
+    const int64_t x = (int64_t)rt.len - rt.n + row / group + 1;
     return (int)(x < 0 ? 0 : x);
   };
   auto lo_of = [&](int hi) { return a.window > 0 && hi > a.window ? hi - a.window : 0; };
   const int hmin = hi_of(rt.row0), hmax = hi_of(last);
   const int lmin = lo_of(hmin), lmax = lo_of(hmax);
+  const int64_t base0 = lmin & ~(kAttnKeys - 1);
+  const uint32_t blocks = a.c.pages > 0 && hmax > lmin ? ((uint32_t)(hmax - base0) + kAttnKeys - 1) / kAttnKeys : 0;
+  const uint32_t per = (blocks + rt.parts - 1) / rt.parts;
+  const uint32_t end = (split + 1) * per < blocks ? (split + 1) * per : blocks;
+  if (a.splits > 1) {
+    const bool empty = split * per >= blocks;
+    note_parts(a, rt, h, M, empty, 64 * WAVES);
+    if (empty) return;
+  }
   int hi[NT], lo[NT];
-  int64_t tok[NT];
-  int head[NT];
-  u32x4_t q[NT][KD];
   float qf[NT], m[NT], l[NT];
   f32x4_t o[NT][KD][2];
 #pragma unroll
   for (int i = 0; i < NT; i++) {
-    const int64_t row = rt.row0 + 16 * i + c;
-    const bool live = row < rt.rows;
-    tok[i] = live ? rt.tok0 + row / a.group : -1;
-    head[i] = h * a.group + (int)(row % a.group);
-    hi[i] = live ? hi_of(row) : 0;
+    // columns past the last row repeat it; their results are not stored
+    const uint32_t row = min(rt.row0 + 16 * i + c, rt.rows - 1), tok = row / group;
+    hi[i] = hi_of(row);
     lo[i] = lo_of(hi[i]);
-    qf[i] = load_query<MODE, D>(a, h, a.q + tok[i] * a.qs + (int64_t)head[i] * D, live, q[i]);
+    const uint16_t* x = a.q + (int64_t)(rt.tok0 + tok) * a.qs +
+                        (int64_t)(h * group + row - tok * group) * D + g * (D / 4);
+    u32x4_t q[KD];
+    qf[i] = load_query<MODE, KD, 8>(a, h, x, q, col_max);
+    if (wave == 0) {
+#pragma unroll
+      for (int st = 0; st < KD; st++) sq[i][st][lane] = q[st];
+    }
     m[i] = -__builtin_inff();
     l[i] = 0.0f;
 #pragma unroll
     for (int T = 0; T < KD; T++) o[i][T][0] = o[i][T][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int64_t base0 = lmin & ~(kAttnKeys - 1);
-  const int64_t blocks = a.c.pages > 0 && hmax > lmin ? (hmax - base0 + kAttnKeys - 1) / kAttnKeys : 0;
-  const int64_t per = (blocks + a.splits - 1) / a.splits;
-  const int64_t end = (split + 1) * per < blocks ? (split + 1) * per : blocks;
-  int64_t blk = split * per + wave;
+  uint32_t blk = split * per + wave;
 
   const float cap_in = a.cap > 0.0f ? 2.0f / a.cap : 0.0f, cap_out = a.cap * kLog2e;
-  auto step = [&](const KvFragment<MODE, D>& f, int64_t base, KvPages pg) {
+  KeyFragment<MODE, D> kf;
+  ValueFragment<MODE, D> vf;
+  auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
+  // one block: its keys and values are in kf and vf; the next block's loads go out
+  // as soon as the registers are free, keys after the first product, values
+  // after the second
+  auto step = [&](int64_t base, KvPages pg, bool more, int64_t next, KvPages npg) {
     f32x4_t s[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; i++)
 #pragma unroll
       for (int t = 0; t < 4; t++) s[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4_t q[NT][KD];
+    int opaque;                          // so that these reads stay in the loop
+    asm volatile("v_mov_b32 %0, %1" : "=v"(opaque) : "v"(lane));
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+      for (int st = 0; st < KD; st++) q[i][st] = sq[i][st][opaque];
     static_for<4>([&](auto tt) {
       constexpr int t = decltype(tt)::value;
       static_for<KD>([&](auto ss) {
         constexpr int st = decltype(ss)::value;
-        const u32x4_t k = key_operand<MODE, st * 8 / KvFragment<MODE, D>::G>(f.k[t][st], f.ks[t]);
+        const u32x4_t k = key_operand<MODE, st * 8 / KeyFragment<MODE, D>::G>(kf.k[t][st], kf.s[t]);
 #pragma unroll
         for (int i = 0; i < NT; i++) s[i][t] = mfma16<MODE>(k, q[i][st], s[i][t]);
       });
     });
-    const bool whole = base >= lmax && base + kAttnKeys <= hmin && __all(pg.v >= 0);
+    if (more) load_keys<MODE, D, WIDE>(a, h, next, npg, kf);
+    float f1[NT];
+#pragma unroll
+    for (int i = 0; i < NT; i++) f1[i] = qf[i];
+    if (a.cap > 0.0f) {
+#pragma unroll
+      for (int i = 0; i < NT; i++) {
+        f1[i] = 1.0f;
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) s[i][t][r] = capped(s[i][t][r] * qf[i], cap_in, cap_out);
+      }
+    }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // bytes of the tokens that count
-    if (!whole) {
+    if (base < lmax || base + kAttnKeys > hmin || !__all(pg.v >= 0)) {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
         keep[t] = 0;
@@ -417,31 +616,20 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
           if (pg.v >= 0 && key >= lmin && key < hmax) keep[t] |= 255u << (8 * r);
 #pragma unroll
           for (int i = 0; i < NT; i++)
-            if (pg.v < 0 || key < lo[i] || key >= hi[i]) s[i][t][r] = -__builtin_inff();
+            s[i][t][r] = pg.v < 0 || key < lo[i] || key >= hi[i] ? -__builtin_inff() : s[i][t][r];
         }
       }
     }
     u32x4_t p[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; i++) {
-      float f1 = qf[i];
-      if (a.cap > 0.0f) {
-#pragma unroll
-        for (int t = 0; t < 4; t++)
-#pragma unroll
-          for (int r = 0; r < 4; r++) {
-            const float x = capped(s[i][t][r] * qf[i], cap_in, cap_out);
-            s[i][t][r] = s[i][t][r] == -__builtin_inff() && !whole ? s[i][t][r] : x;
-          }
-        f1 = 1.0f;
-      }
       float mx = s[i][0][0];
 #pragma unroll
       for (int t = 0; t < 4; t++)
 #pragma unroll
         for (int r = 0; r < 4; r++) mx = fmaxf(mx, s[i][t][r]);
-      mx = fmaxf(m[i], col_max(mx) * f1);
-      if (__any(mx > m[i])) {
+      mx = fmaxf(m[i], col_max(mx) * f1[i]);
+      if (__any(mx > m[i] + kLag)) {
         const float fac = mx > m[i] ? __builtin_amdgcn_exp2f(m[i] - mx) : 1.0f;
         l[i] *= fac;
 #pragma unroll
@@ -459,7 +647,7 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
         float e[4];
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][t][r], f1, -ref));
+          e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][t][r], f1[i], -ref));
           l[i] += e[r];
         }
         if constexpr (MODE == 2) {
@@ -476,43 +664,29 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         u32x4_t even, odd;
-        value_operands<MODE>(f.v[T][2 * u], f.v[T][2 * u + 1], f.vs[T][2 * u] & keep[2 * u],
-                             f.vs[T][2 * u + 1] & keep[2 * u + 1], even, odd);
+        value_operands<MODE>(vf.v[T][2 * u], vf.v[T][2 * u + 1], vf.s[T][2 * u] & keep[2 * u],
+                             vf.s[T][2 * u + 1] & keep[2 * u + 1], even, odd);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
           o[i][T][0] = mfma16<MODE>(even, p[i][u], o[i][T][0]);
           o[i][T][1] = mfma16<MODE>(odd, p[i][u], o[i][T][1]);
         }
       }
+    if (more) load_values<MODE, D, WIDE>(a, h, next, npg, vf);
   };
 
-  // two fragments in turn: the next block's loads are under way while this one is used
+  __syncthreads();                       // the queries are in LDS
   if (blk < end) {
-    KvFragment<MODE, D> f0, f1;
-    auto base_of = [&](int64_t i) { return base0 + i * kAttnKeys; };
-    KvPages p0 = load_pages(a, rt.b, base_of(blk)), p1 = load_pages(a, rt.b, base_of(blk + WAVES));
-    load_kv<MODE, D>(a, h, base_of(blk), p0, f0);
-    while (true) {
-      const bool more = blk + WAVES < end;
-      KvPages p2 = p1;
-      if (more) {
-        load_kv<MODE, D>(a, h, base_of(blk + WAVES), p1, f1);
-        p2 = load_pages(a, rt.b, base_of(blk + 2 * WAVES));
-      }
-      step(f0, base_of(blk), p0);
-      blk += WAVES;
-      if (!more) break;
-      const bool again = blk + WAVES < end;
-      KvPages p3 = p2;
-      if (again) {
-        load_kv<MODE, D>(a, h, base_of(blk + WAVES), p2, f0);
-        p3 = load_pages(a, rt.b, base_of(blk + 2 * WAVES));
-      }
-      step(f1, base_of(blk), p1);
-      blk += WAVES;
-      if (!again) break;
-      p0 = p2;
-      p1 = p3;
+    KvPages pg = load_pages<WIDE>(a, rt.b, base_of(blk));
+    KvPages npg = load_pages<WIDE>(a, rt.b, base_of(blk + WAVES));
+    load_keys<MODE, D, WIDE>(a, h, base_of(blk), pg, kf);
+    __builtin_amdgcn_sched_barrier(0);   // keys first, as in the loop: its waits count on it
+    load_values<MODE, D, WIDE>(a, h, base_of(blk), pg, vf);
+    for (; blk < end; blk += WAVES) {
+      const KvPages after = load_pages<WIDE>(a, rt.b, base_of(blk + 2 * WAVES));
+      step(base_of(blk), pg, blk + WAVES < end, base_of(blk + WAVES), npg);
+      pg = npg;
+      npg = after;
     }
   }
 
@@ -542,7 +716,7 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
     constexpr int LANES = D / PER;                    // lanes per row
     const int row = (int)threadIdx.x / LANES, part = (int)threadIdx.x % LANES;
     for (int rr = row; rr < 16; rr += 64 * WAVES / LANES) {
-      const int64_t full = rt.row0 + 16 * i + rr;
+      const uint32_t full = rt.row0 + 16 * i + rr;
       if (full >= rt.rows) break;
       float mw[WAVES], ll = 0.0f, top = -__builtin_inff();
 #pragma unroll
@@ -550,8 +724,8 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
 #pragma unroll
       for (int w = 0; w < WAVES; w++)
         ll += sm[w][rr][1] * (mw[w] == top ? 1.0f : __builtin_amdgcn_exp2f(mw[w] - top));
-      const int64_t tk = rt.tok0 + full / a.group;
-      const int hd = h * a.group + (int)(full % a.group);
+      const int64_t tk = rt.tok0 + full / group;
+      const int hd = (int)(h * group + full % group);
       const float va = MODE == 2 ? 1.0f : a.c.vam[h] / (6.0f * (MODE == 1 ? 256.0f : 448.0f));
       const float inv = ll == 0.0f ? 0.0f : va / ll;
       const int64_t at = ((int64_t)split * a.tokens + tk) * a.hq + hd;
@@ -582,16 +756,17 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NT == 1 ? 2 : 1) void kv_att
   }
 }
 
-// Joins the parts of the context: D/4 lanes (16 bytes each) times `parts`
-// (a power of two) for a query row, the parts taking the splits in turn.
+// Joins the parts of the context: D/4 lanes (16 bytes each) times
+// `groups` (a power of two) for a query row, the groups taking its parts in
+// turn.
 template <int MODE, int D>
-__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int parts) {
+__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int groups) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f;
   constexpr int L = D / 4;
   __shared__ float4 sx[kThreads];
   __shared__ float2 sm[kThreads];
-  const int t = (int)threadIdx.x, lane = t % L, part = t / L % parts;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / (L * parts)) + t / (L * parts);
+  const int t = (int)threadIdx.x, lane = t % L, grp = t / L % groups;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / (L * groups)) + t / (L * groups);
   const int64_t rows = a.tokens * a.hq;
   const bool live = row < rows;
   float top = -__builtin_inff(), l = 0.0f, x[4] = {};
@@ -607,25 +782,27 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
     top = mm;
   };
   if (live) {
+    const int n = a.parts[row];
 #pragma unroll 4
-    for (int s = part; s < a.splits; s += parts) {
+    for (int s = grp; s < n; s += groups) {
       const float2 ml = *(const float2*)(a.pm + (s * rows + row) * 2);
-      const float4 y = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
+      float4 y = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
+      if (ml.y == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // its sums were not written
       add(ml.x, ml.y, y);
     }
   }
-  if (parts > 1) {
-    for (int half = parts / 2; half > 0; half >>= 1) {
+  if (groups > 1) {
+    for (int half = groups / 2; half > 0; half >>= 1) {
       __syncthreads();
       sx[t] = make_float4(x[0], x[1], x[2], x[3]);
       sm[t] = make_float2(top, l);
       __syncthreads();
-      if (part < half) add(sm[t + half * L].x, sm[t + half * L].y, sx[t + half * L]);
+      if (grp < half) add(sm[t + half * L].x, sm[t + half * L].y, sx[t + half * L]);
     }
   }
-  if (!live || part) return;
-  const int64_t tok = row / a.hq;
-  const int head = (int)(row - tok * a.hq), h = head / a.group;
+  if (!live || grp) return;
+  const int64_t tok = (uint32_t)row / (uint32_t)a.hq;
+  const int head = (int)(row - tok * a.hq), h = (int)((uint32_t)head / (uint32_t)a.group);
   const float va = MODE == 2 ? 1.0f : a.c.vam[h] / (6.0f * (MODE == 1 ? 256.0f : 448.0f));
   const float inv = l == 0.0f ? 0.0f : va / l;
   *(uint2*)(a.out + tok * a.os + (int64_t)head * D + lane * 4) =

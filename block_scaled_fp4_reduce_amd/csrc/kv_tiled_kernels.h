@@ -66,7 +66,7 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* o) {
 }
 
 template <int MODE, int D>
-__device__ __forceinline__ KvPages tile_pages(const AttnArgs& a, int64_t b, int64_t base) {
+__device__ __forceinline__ KvPages tile_pages(const AttnArgs& a, uint32_t b, int64_t base) {
   using C = TileCodes<MODE, D>;
   const int t = (int)threadIdx.x;
   KvPages p;
@@ -162,71 +162,53 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 template <int MODE, int D>
-__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(AttnArgs a, uint32_t tiles) {
-  constexpr float kOff = MODE == 2 ? 0.0f : 12.0f;
+__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(AttnArgs a) {
+  constexpr float kOff = MODE == 2 ? 0.0f : 12.0f, kLag = MODE == 2 ? 8.0f : 3.0f;
   constexpr int QS = D / 16, NT = D / 32;
   using L = TileLds<D>;
   __shared__ __align__(16) L lds;
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int c = lane & 31, hh = lane >> 5;
-  uint32_t id = blockIdx.x;
-  const int h = (int)(id % (uint32_t)a.c.heads);
-  id /= (uint32_t)a.c.heads;
-  const int split = (int)(id % (uint32_t)a.splits);
-  RowTile rt;
-  // late rows see the most keys: they start first
-  if (!row_tile(a, tiles - 1 - id / (uint32_t)a.splits, kTileRows, rt)) return;
-  auto hi_of = [&](int64_t row) {
-    const int64_t x = rt.len - rt.n + row / a.group + 1;
+  // from the last place on: late rows see the most keys, so they start first
+  const uint32_t place = blockIdx.x / (uint32_t)a.c.heads;
+  const int h = (int)(blockIdx.x - place * (uint32_t)a.c.heads);
+  Work rt;
+  if (!find_work<kTileRows>(a, gridDim.x / (uint32_t)a.c.heads - 1 - place, rt)) return;
+  const int split = (int)rt.split;
+  const uint32_t group = (uint32_t)a.group;
+  auto hi_of = [&](uint32_t row) {
+    const int64_t x = (int64_t)rt.len - rt.n + row / group + 1;
     return (int)(x < 0 ? 0 : x);
   };
   auto lo_of = [&](int hi) { return a.window > 0 && hi > a.window ? hi - a.window : 0; };
-  auto end_of = [&](int64_t row) { return row < rt.rows ? row : rt.rows - 1; };
+  auto end_of = [&](uint32_t row) { return row < rt.rows ? row : rt.rows - 1; };
   const int tlo = lo_of(hi_of(rt.row0)), thi = hi_of(end_of(rt.row0 + kTileRows - 1));
-  const int64_t w0 = rt.row0 + 32 * wave;
+  const int64_t base0 = tlo & ~(kAttnKeys - 1);
+  const uint32_t blocks =
+      a.c.pages > 0 && thi > tlo ? ((uint32_t)(thi - base0) + kAttnKeys - 1) / kAttnKeys : 0;
+  const uint32_t per = (blocks + rt.parts - 1) / rt.parts;
+  const uint32_t first = split * per;
+  const uint32_t end = first + per < blocks ? first + per : blocks;
+  if (a.splits > 1) {
+    const bool empty = first >= blocks;
+    note_parts(a, rt, h, kTileRows, empty, kThreads);
+    if (empty) return;
+  }
+  const uint32_t w0 = rt.row0 + 32 * wave;
   const bool alive = w0 < rt.rows;
   const int whmin = hi_of(end_of(w0)), whmax = alive ? hi_of(end_of(w0 + 31)) : 0;
   const int wlmin = lo_of(whmin), wlmax = lo_of(whmax);
-  const int64_t row = w0 + c;
-  const bool live = row < rt.rows;
-  const int64_t tok = live ? rt.tok0 + row / a.group : 0;
-  const int head = h * a.group + (int)(row % a.group);
-  const int hi = live ? hi_of(row) : 0, lo = lo_of(hi);
+  const bool live = w0 + c < rt.rows;
+  const uint32_t row = end_of(w0 + c);   // columns past the last row repeat it, unstored
+  const int64_t tok = rt.tok0 + row / group;
+  const int head = (int)(h * group + row % group);
+  const int hi = hi_of(row), lo = lo_of(hi);
 
   // queries: step s, slot j is channel 16 s + 8 hh + j
   u32x4_t q[QS];
-  float qf;
-  {
-    const uint16_t* x = a.q + tok * a.qs + (int64_t)head * D + 8 * hh;
-    const float k = fabsf(a.scale) * kLog2e;
-    const bool on = live && a.scale != 0.0f;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-    uint32_t mx = 0;
-#pragma unroll
-    for (int s = 0; s < QS; s++) {
-      q[s] = on ? *(const u32x4_t*)(x + 16 * s) ^ flip : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const uint32_t y = q[s][i] & 0x7FFF7FFFu;
-        mx = max(mx, max(y & 0xFFFFu, y >> 16));
-      }
-    }
-    if constexpr (MODE == 2) {
-      qf = fmaxf(k, 0x1p-126f);
-    } else {
-      const float m = half_max(__uint_as_float(mx << 16));
-      int shift = 141 - (int)(__float_as_uint(m) >> 23);         // 2^14 <= m 2^shift < 2^15
-      shift = shift > 127 ? 127 : shift;
-#pragma unroll
-      for (int s = 0; s < QS; s++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          q[s][i] = bits_of(f16x2_t{(_Float16)__builtin_ldexpf(bf16_lo(q[s][i]), shift),
-                                    (_Float16)__builtin_ldexpf(bf16_hi(q[s][i]), shift)});
-      const float alpha = a.c.kam[h] / (6.0f * (MODE == 1 ? 256.0f : 448.0f));
-      qf = fmaxf(__builtin_ldexpf(k * alpha, -shift), 0x1p-126f);
-    }
-  }
+  const float qf = load_query<MODE, QS, 16>(
+      a, h, a.q + tok * a.qs + (int64_t)head * D + 8 * hh, q, half_max);
 
   float m = -__builtin_inff(), l = 0.0f;
   f32x16_t o[NT];
@@ -250,28 +232,24 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
         s[kt] = mfma32<MODE>(k, q[st], s[kt]);
       }
     }
+    float f1 = qf;
+    if (a.cap > 0.0f) {
+      f1 = 1.0f;
+#pragma unroll
+      for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) s[kt][r] = capped(s[kt][r] * qf, cap_in, cap_out);
+    }
     const int4 ok = *(const int4*)lds.ok[buf];
-    const bool whole = base >= wlmax && base + 64 <= whmin && (ok.x & ok.y & ok.z & ok.w);
-    if (!whole) {
+    if (base < wlmax || base + 64 > whmin || !(ok.x & ok.y & ok.z & ok.w)) {
       const int oks[4] = {ok.x, ok.y, ok.z, ok.w};
 #pragma unroll
       for (int kt = 0; kt < 2; kt++)
 #pragma unroll
         for (int r = 0; r < 16; r++) {
           const int key = (int)base + 32 * kt + 16 * (r >> 3) + 8 * hh + (r & 7);
-          if (!oks[2 * kt + (r >> 3)] || key < lo || key >= hi) s[kt][r] = -__builtin_inff();
+          s[kt][r] = !oks[2 * kt + (r >> 3)] || key < lo || key >= hi ? -__builtin_inff() : s[kt][r];
         }
-    }
-    float f1 = qf;
-    if (a.cap > 0.0f) {
-#pragma unroll
-      for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-          const float x = capped(s[kt][r] * qf, cap_in, cap_out);
-          s[kt][r] = s[kt][r] == -__builtin_inff() && !whole ? s[kt][r] : x;
-        }
-      f1 = 1.0f;
     }
     float mx = s[0][0];
 #pragma unroll
@@ -279,7 +257,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
 #pragma unroll
       for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[kt][r]);
     mx = fmaxf(m, half_max(mx) * f1);
-    if (__any(mx > m)) {
+    if (__any(mx > m + kLag)) {
       const float fac = mx > m ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
       l *= fac;
 #pragma unroll
@@ -312,13 +290,8 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
       }
   };
 
-  const int64_t base0 = tlo & ~(kAttnKeys - 1);
-  const int64_t blocks = a.c.pages > 0 && thi > tlo ? (thi - base0 + kAttnKeys - 1) / kAttnKeys : 0;
-  const int64_t per = (blocks + a.splits - 1) / a.splits;
-  const int64_t first = split * per;
-  const int64_t end = first + per < blocks ? first + per : blocks;
   if (first < end) {
-    auto base_of = [&](int64_t i) { return base0 + i * kAttnKeys; };
+    auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
     TileCodes<MODE, D> f;
     KvPages pg = tile_pages<MODE, D>(a, rt.b, base_of(first));
     load_tile<MODE, D>(a, h, base_of(first), pg, f);
@@ -326,14 +299,15 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
     store_tile<MODE, D>(f, base_of(first), tlo, thi, lds, 0);
     if (first + 1 < end) load_tile<MODE, D>(a, h, base_of(first + 1), pg, f);
     pg = tile_pages<MODE, D>(a, rt.b, base_of(first + 2));
-    for (int64_t i = first; i < end; i++) {
+    for (uint32_t i = first; i < end; i++) {
       const int buf = (int)(i - first) & 1;
       __syncthreads();                   // tile i is decoded; the other buffer is free
       if (i + 1 < end) {
         store_tile<MODE, D>(f, base_of(i + 1), tlo, thi, lds, buf ^ 1);
         if (i + 2 < end) {
+          const KvPages next = tile_pages<MODE, D>(a, rt.b, base_of(i + 3));
           load_tile<MODE, D>(a, h, base_of(i + 2), pg, f);
-          pg = tile_pages<MODE, D>(a, rt.b, base_of(i + 3));
+          pg = next;
         }
       }
       const int64_t base = base_of(i);
