@@ -15,6 +15,7 @@ Two layers:
 from __future__ import annotations
 
 import ctypes as C
+import importlib
 import os
 
 FOUR_OVER_SIX = 1 << 0
@@ -348,31 +349,17 @@ def fp4_dequantize(fmt, codes, scales, alpha, rows, cols, flags=0, out=None, str
 
 
 # ------------------------------------------------------------------ FP4 key/value cache
-def _scratch(nbytes, device, stream):
-    """Workspace from torch's allocator, held back from reuse until the work
-    queued on an explicit stream is done."""
-    torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        ws.record_stream(stream)
-    return ws
+_native = None
 
 
-def _heads(x, heads, dim, what):
-    """Token stride of x [tokens][heads][dim] bf16 on the GPU, each token's heads in one run."""
-    torch = _torch()
-    if x.dtype != torch.bfloat16:
-        raise TypeError("%s must be bfloat16, got %s" % (what, x.dtype))
-    if not x.is_cuda or x.dim() != 3 or (heads is not None and x.shape[1] != heads) or \
-            x.shape[2] != dim:
-        raise ValueError("%s must be a GPU tensor [tokens][%s][%d], got %s" % (
-            what, "heads" if heads is None else heads, dim, tuple(x.shape)))
-    st, sh, sd = x.stride()
-    if x.shape[0] and ((x.shape[1] > 1 and sh != dim) or sd != 1):
-        raise ValueError("%s: a token's heads must be contiguous" % what)
-    return st if x.shape[0] > 1 else x.shape[1] * dim
+def _binding():
+    """The compiled binding of these calls (built beside libfp4q.so)."""
+    global _native
+    if _native is None:
+        lib()                                # a missing build is reported there
+        _torch()                             # the binding links to torch's libraries
+        _native = importlib.import_module(__name__ + "._calls")
+    return _native
 
 
 def _ints(x, dtype, shape, what):
@@ -390,7 +377,7 @@ class KvCache:
     the constructor takes a program's own."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_amax", "v_amax", "fmt", "flags",
-                 "pages", "heads", "page_size", "head_dim", "_c")
+                 "pages", "heads", "page_size", "head_dim", "_c", "_at")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_amax=None, v_amax=None,
                  fmt=FORMAT_NVFP4, flags=0):
@@ -414,6 +401,7 @@ class KvCache:
         self._c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                           v_scales.data_ptr(), _ptr(k_amax), _ptr(v_amax), pages, page_size, heads,
                           dim, fmt, flags)
+        self._at = C.addressof(self._c)
 
     @classmethod
     def alloc(cls, pages, page_size, heads, head_dim, fmt=FORMAT_NVFP4, flags=0, k_amax=None,
@@ -432,54 +420,20 @@ def fp4_kv_write(cache, k, v, slots, stream=None):
     """Quantize keys and values [tokens][heads][head_dim] (bf16) into ``cache``
     at ``slots`` [tokens] (int64; slot s is token s % page_size of page
     s / page_size).  Slots outside the cache are skipped."""
-    torch = _torch()
-    ks = _heads(k, cache.heads, cache.head_dim, "k")
-    vs = _heads(v, cache.heads, cache.head_dim, "v")
-    if v.shape[0] != k.shape[0]:
-        raise ValueError("k and v disagree on the number of tokens")
-    at = _ints(slots, torch.int64, (k.shape[0],), "slots")
-    _check("fp4_kv_write", lib().fp4_kv_write(cache._c, k.data_ptr(), ks, v.data_ptr(), vs, at,
-                                              k.shape[0], _stream(stream)))
+    _binding().kv_write(cache._at, k, v, slots, stream)
 
 
 def fp4_kv_read(cache, slots, out=None, stream=None):
     """The keys and values at ``slots`` [tokens] as bf16 (k, v), each
     [tokens][heads][head_dim]; ``out`` may supply them."""
-    torch = _torch()
-    n = slots.shape[0]
-    if out is None:
-        shape = (n, cache.heads, cache.head_dim)
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=slots.device),
-               torch.empty(shape, dtype=torch.bfloat16, device=slots.device))
-    k, v = out
-    ks = _heads(k, cache.heads, cache.head_dim, "k")
-    vs = _heads(v, cache.heads, cache.head_dim, "v")
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ValueError("k, v and slots disagree on the number of tokens")
-    at = _ints(slots, torch.int64, (n,), "slots")
-    _check("fp4_kv_read", lib().fp4_kv_read(cache._c, at, n, k.data_ptr(), ks, v.data_ptr(), vs,
-                                            _stream(stream)))
-    return k, v
+    return _binding().kv_read(cache._at, slots, out, stream)
 
 
-def _queries(cache, q, page_table, kv_lens, cu_q, max_q, scale, softcap, window):
-    torch = _torch()
-    qs = _heads(q, None, cache.head_dim, "q")
-    seqs = kv_lens.shape[0]
-    lens = _ints(kv_lens, torch.int32, (seqs,), "kv_lens")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [seqs][pages of the longest]")
-    table = _ints(page_table, torch.int32, (seqs, page_table.shape[1]), "page_table")
-    cu = None if cu_q is None else _ints(cu_q, torch.int32, (seqs + 1,), "cu_q")
-    return _CQueries(q.data_ptr(), qs, q.shape[0], seqs, cu, max_q, lens, table,
-                     page_table.shape[1], q.shape[1], window,
-                     cache.head_dim ** -0.5 if scale is None else scale, softcap)
-
-
-def fp4_kv_attention_workspace_bytes(cache, q, page_table, kv_lens, cu_q=None, max_q=0):
+def fp4_kv_attention_workspace_bytes(cache, q, page_table, kv_lens, cu_q=None, max_q=0, scale=None,
+                                     softcap=0.0, window=0):
     """Bytes of workspace of ``fp4_kv_attention`` on these arguments."""
-    x = _queries(cache, q, page_table, kv_lens, cu_q, max_q, None, 0.0, 0)
-    return int(lib().fp4_kv_attention_workspace_bytes(cache._c, x))
+    return _binding().kv_attention_ws(cache._at, q, page_table, kv_lens, cu_q, max_q, scale,
+                                      softcap, window)
 
 
 def fp4_kv_attention(cache, q, page_table, kv_lens, cu_q=None, max_q=0, scale=None, softcap=0.0,
@@ -493,25 +447,8 @@ def fp4_kv_attention(cache, q, page_table, kv_lens, cu_q=None, max_q=0, scale=No
     sequence's pages.  max_q is the largest number of new tokens where the
     program knows it (0: not known).  Returns out (bf16, like q), or
     (out, lse) with lse [tokens][q_heads] float32."""
-    torch = _torch()
-    x = _queries(cache, q, page_table, kv_lens, cu_q, max_q, scale, softcap, window)
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    os_ = _heads(out, q.shape[1], cache.head_dim, "out")
-    if out.shape[0] != q.shape[0]:
-        raise ValueError("out and q disagree on the number of tokens")
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _ints(lse, torch.float32, q.shape[:2], "lse")
-    L = lib()
-    if ws is None:
-        need = L.fp4_kv_attention_workspace_bytes(cache._c, x)
-        ws = _scratch(need, q.device, stream) if need else None
-    _check("fp4_kv_attention", L.fp4_kv_attention(
-        cache._c, x, out.data_ptr(), os_, _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
-        _stream(stream)))
-    return out if lse is None else (out, lse)
+    return _binding().kv_attention(cache._at, q, page_table, kv_lens, cu_q, max_q, scale, softcap,
+                                   window, want_lse, out, lse, ws, stream)
 
 
 # ------------------------------------------------------------------ norm + rotation
@@ -525,36 +462,6 @@ def rope_table(positions, rot_dim, base=10000.0, device="cuda"):
     return torch.stack((angle.cos(), angle.sin()), -1).float().contiguous()
 
 
-def _rope(q, k, q_weight, k_weight, positions, table, eps, interleaved):
-    torch = _torch()
-    tokens, dim = q.shape[0], q.shape[2]
-    qs, ks = _heads(q, None, dim, "q"), _heads(k, None, dim, "k")
-    if k.shape[0] != tokens:
-        raise ValueError("q and k disagree on the number of tokens")
-    w = []
-    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        w.append(None if t is None else _ints(t, torch.bfloat16, (dim,), what))
-    pos = _ints(positions, torch.int64, (tokens,), "positions")
-    if table.dim() != 3:
-        raise ValueError("table must be [positions][rot_dim/2][2]")
-    cs = _ints(table, torch.float32, (table.shape[0], table.shape[1], 2), "table")
-    return _CRope(q.data_ptr(), k.data_ptr(), qs, ks, tokens, w[0], w[1], pos, cs, table.shape[0],
-                  q.shape[1], k.shape[1], dim, 2 * table.shape[1], eps,
-                  ROPE_INTERLEAVED if interleaved else 0)
-
-
-def _like(t, x, what):
-    """Token stride of t, shaped like x; a new tensor where t is None."""
-    torch = _torch()
-    if t is None:
-        t = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        return t, x.shape[1] * x.shape[2]
-    st = _heads(t, x.shape[1], x.shape[2], what)
-    if t.shape[0] != x.shape[0]:
-        raise ValueError("%s has another number of tokens" % what)
-    return t, st
-
-
 def qk_norm_rope(q, k, q_weight, k_weight, positions, table, eps=1e-6, interleaved=False, out=None,
                  stream=None):
     """RMS norm of each head of q and k ([tokens][heads][head_dim] bf16) with
@@ -562,13 +469,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, table, eps=1e-6, interleav
     first 2 * table.shape[1] values by the angles of ``positions`` [tokens]
     (int64) in ``table`` (``rope_table``).  Returns (q, k); ``out`` may supply
     them and may be (q, k) themselves."""
-    x = _rope(q, k, q_weight, k_weight, positions, table, eps, interleaved)
-    oq, ok = (None, None) if out is None else out
-    oq, qs = _like(oq, q, "out q")
-    ok, ks = _like(ok, k, "out k")
-    _check("qk_norm_rope", lib().qk_norm_rope(x, oq.data_ptr(), qs, ok.data_ptr(), ks,
-                                              _stream(stream)))
-    return oq, ok
+    return _binding().norm_rope(q, k, q_weight, k_weight, positions, table, eps, interleaved, out,
+                                stream)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, table, eps=1e-6,
@@ -576,19 +478,5 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, t
     """Gradients of ``qk_norm_rope`` on the same arguments: (dq, dk, dq_weight,
     dk_weight), dq and dk bf16 (``out`` may supply them), the weights' float32
     [head_dim] (None without a weight)."""
-    torch = _torch()
-    x = _rope(q, k, q_weight, k_weight, positions, table, eps, interleaved)
-    gq, gqs = _like(dq_out, q, "dq_out")
-    gk, gks = _like(dk_out, k, "dk_out")
-    dq, dk = (None, None) if out is None else out
-    dq, qs = _like(dq, q, "out dq")
-    dk, ks = _like(dk, k, "out dk")
-    dim = q.shape[2]
-    new = lambda w: None if w is None else torch.empty(dim, dtype=torch.float32, device=q.device)
-    dqw, dkw = new(q_weight), new(k_weight)
-    if ws is None and not (dqw is None and dkw is None):
-        ws = _scratch(lib().qk_norm_rope_workspace_bytes(dim), q.device, stream)
-    _check("qk_norm_rope_backward", lib().qk_norm_rope_backward(
-        x, gq.data_ptr(), gqs, gk.data_ptr(), gks, dq.data_ptr(), qs, dk.data_ptr(), ks, _ptr(dqw),
-        _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
-    return dq, dk, dqw, dkw
+    return _binding().norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, table,
+                                         eps, interleaved, out, ws, stream)

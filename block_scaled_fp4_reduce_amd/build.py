@@ -1,4 +1,5 @@
-"""Build libfp4q.so (HIP, gfx950) in-tree with hipcc.
+"""Build libfp4q.so (HIP, gfx950) in-tree with hipcc, and beside it the Python
+binding _calls.so (host C++ against torch's headers).
 
     python -m block_scaled_fp4_reduce_amd.build [--asm]
 
@@ -9,13 +10,16 @@ packed fp32 instructions disabled; fp32 division stays correctly rounded
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4q.so")
+BINDING = os.path.join(HERE, "_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -34,6 +38,18 @@ def deps():
     out = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     out.append(os.path.join(os.path.dirname(HERE), "include", "fp4q.h"))
     return out
+
+
+def binding_command(out):
+    """g++ command of the binding, linked to the libfp4q.so beside it."""
+    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+           "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", *["-isystem" + i for i in inc],
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + HERE, "-lfp4q",
+            "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_hip",
+            "-ltorch_cpu", "-ltorch_python"]
 
 
 def build(verbose: bool = False) -> str:
@@ -55,17 +71,22 @@ def build(verbose: bool = False) -> str:
             print(" ".join(link), flush=True)
         subprocess.check_call(link)
         os.replace(tmp, LIB)
+        cmd = binding_command(tmp)       # links to the library, so it comes after
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+        os.replace(tmp, BINDING)
     finally:
-        for f in objs:
+        for f in [*objs, tmp]:
             if os.path.exists(f):
                 os.remove(f)
     return LIB
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in deps())
 
 
