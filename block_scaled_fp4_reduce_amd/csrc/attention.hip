@@ -188,11 +188,12 @@ size_t attention_ws(const fp4_kv_cache* c, const fp4_kv_queries* x, const AttnPl
 template <int MODE, int D>
 hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)(p.places * a.c.heads);
+  const bool wide = a.c.page_shift >= 6;   // a block of 64 keys lies in one page
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
-    e = launch(kv_tiled_kernel<MODE, D>, grid, kThreads, st, a);
+    e = wide ? launch(kv_tiled_kernel<MODE, D, true>, grid, kThreads, st, a)
+             : launch(kv_tiled_kernel<MODE, D, false>, grid, kThreads, st, a);
   } else {
-    const bool wide = a.c.page_shift >= 6;
     auto go = [&](auto nt) {
       constexpr int N = decltype(nt)::value;
       return wide ? launch(kv_attention_kernel<MODE, D, N, 4, true>, grid, 256, st, a)

@@ -491,10 +491,24 @@ __device__ __forceinline__ float load_query(const AttnArgs& a, int h, const uint
   }
 }
 
-// c tanh(s / c) of a score in powers of two: tanh y = 1 - 2 / (exp(2 y) + 1).
-__device__ __forceinline__ float capped(float s, float in, float out) {
-  const float e = __builtin_amdgcn_exp2f(s * in);    // in = 2 / c (s is in powers of two)
-  return out - 2.0f * out * __builtin_amdgcn_rcpf(e + 1.0f);
+// Scores from the products x: in powers of two, s = f x + off with f > 0, so
+// that maxima can be taken of x and the weight is one fma and one exponential.
+// Capped ones, c tanh(s / c) = c - 2 c / (exp(2 s / c) + 1), have
+// x = -1 / (exp + 1) in place of the product, f = 2 c and off = c.
+struct ScoreScale {
+  float f, off, in;                      // in > 0: capped
+};
+__device__ __forceinline__ ScoreScale score_scale(const AttnArgs& a, float qf) {
+  ScoreScale s{qf, 0.0f, 0.0f};
+  if (a.cap > 0.0f) {
+    s.in = qf * (2.0f / a.cap);          // a score in powers of two, s / c ln 2 of its tanh's
+    s.f = 2.0f * a.cap * kLog2e;
+    s.off = a.cap * kLog2e;
+  }
+  return s;
+}
+__device__ __forceinline__ float capped(float x, float in) {
+  return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x * in));
 }
 
 // NT columns of 16 query rows, WAVES waves that take the blocks of 64 keys of
@@ -539,7 +553,8 @@ void kv_attention_kernel(AttnArgs a) {
     if (empty) return;
   }
   int hi[NT], lo[NT];
-  float qf[NT], m[NT], l[NT];
+  ScoreScale sc[NT];
+  float m[NT], l[NT];
   f32x4_t o[NT][KD][2];
 #pragma unroll
   for (int i = 0; i < NT; i++) {
@@ -550,7 +565,7 @@ void kv_attention_kernel(AttnArgs a) {
     const uint16_t* x = a.q + (int64_t)(rt.tok0 + tok) * a.qs +
                         (int64_t)(h * group + row - tok * group) * D + g * (D / 4);
     u32x4_t q[KD];
-    qf[i] = load_query<MODE, KD, 8>(a, h, x, q, col_max);
+    sc[i] = score_scale(a, load_query<MODE, KD, 8>(a, h, x, q, col_max));
     if (wave == 0) {
 #pragma unroll
       for (int st = 0; st < KD; st++) sq[i][st][lane] = q[st];
@@ -562,7 +577,6 @@ void kv_attention_kernel(AttnArgs a) {
   }
   uint32_t blk = split * per + wave;
 
-  const float cap_in = a.cap > 0.0f ? 2.0f / a.cap : 0.0f, cap_out = a.cap * kLog2e;
   KeyFragment<MODE, D> kf;
   ValueFragment<MODE, D> vf;
   auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
@@ -592,18 +606,13 @@ void kv_attention_kernel(AttnArgs a) {
       });
     });
     if (more) load_keys<MODE, D, WIDE>(a, h, next, npg, kf);
-    float f1[NT];
-#pragma unroll
-    for (int i = 0; i < NT; i++) f1[i] = qf[i];
     if (a.cap > 0.0f) {
 #pragma unroll
-      for (int i = 0; i < NT; i++) {
-        f1[i] = 1.0f;
+      for (int i = 0; i < NT; i++)
 #pragma unroll
         for (int t = 0; t < 4; t++)
 #pragma unroll
-          for (int r = 0; r < 4; r++) s[i][t][r] = capped(s[i][t][r] * qf[i], cap_in, cap_out);
-      }
+          for (int r = 0; r < 4; r++) s[i][t][r] = capped(s[i][t][r], sc[i].in);
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // bytes of the tokens that count
     if (base < lmax || base + kAttnKeys > hmin || !__all(pg.v >= 0)) {
@@ -628,7 +637,7 @@ void kv_attention_kernel(AttnArgs a) {
       for (int t = 0; t < 4; t++)
 #pragma unroll
         for (int r = 0; r < 4; r++) mx = fmaxf(mx, s[i][t][r]);
-      mx = fmaxf(m[i], col_max(mx) * f1[i]);
+      mx = fmaxf(m[i], __builtin_fmaf(col_max(mx), sc[i].f, sc[i].off));
       if (__any(mx > m[i] + kLag)) {
         const float fac = mx > m[i] ? __builtin_amdgcn_exp2f(m[i] - mx) : 1.0f;
         l[i] *= fac;
@@ -641,13 +650,13 @@ void kv_attention_kernel(AttnArgs a) {
           }
         m[i] = mx;
       }
-      const float ref = (m[i] == -__builtin_inff() ? 0.0f : m[i]) - kOff;
+      const float ref = (m[i] == -__builtin_inff() ? 0.0f : m[i]) - kOff - sc[i].off;
 #pragma unroll
       for (int t = 0; t < 4; t++) {
         float e[4];
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][t][r], f1[i], -ref));
+          e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][t][r], sc[i].f, -ref));
           l[i] += e[r];
         }
         if constexpr (MODE == 2) {

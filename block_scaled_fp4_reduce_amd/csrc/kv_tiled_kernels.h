@@ -49,55 +49,51 @@ struct TileCodes {
   int kpage, vpage;
 };
 
-template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* o) {
-  if constexpr (N == 2) {
-    const u32x2_t w = *(const u32x2_t*)p;
-    o[0] = w[0];
-    o[1] = w[1];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const u32x4_t w = *(const u32x4_t*)(p + 4 * i);
-#pragma unroll
-      for (int e = 0; e < 4; e++) o[i + e] = w[e];
-    }
-  }
-}
-
-template <int MODE, int D>
+template <int MODE, int D, bool WIDE>
 __device__ __forceinline__ KvPages tile_pages(const AttnArgs& a, uint32_t b, int64_t base) {
   using C = TileCodes<MODE, D>;
   const int t = (int)threadIdx.x;
   KvPages p;
-  p.k = page_id(a, b, base + (t >> 2));
-  p.v = page_id(a, b, base + (t % C::TG) * C::TOK);
+  p.k = page_id(a, b, WIDE ? base : base + (t >> 2));
+  p.v = WIDE ? p.k : page_id(a, b, base + (t % C::TG) * C::TOK);
   return p;
 }
 
-template <int MODE, int D>
+template <int MODE, int D, bool WIDE>
 __device__ __forceinline__ void load_tile(const AttnArgs& a, int h, int64_t base, KvPages pg,
                                           TileCodes<MODE, D>& f) {
   using C = TileCodes<MODE, D>;
-  constexpr int G = C::G;
-  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift;
+  constexpr int G = C::G, KB = C::KW * 4 > 16 ? 16 : C::KW * 4, VB = C::VW * 4;
+  constexpr int SB = D / 4 >= G ? D / 4 / G : 1;
+  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, part = t & 3;
   f.kpage = pg.k;
   f.vpage = pg.v;
   const int64_t pk = (int64_t)(pg.k < 0 ? 0 : pg.k) * a.c.heads + h;
   const int64_t pv = (int64_t)(pg.v < 0 ? 0 : pg.v) * a.c.heads + h;
-  const int ak = (int)(base + (t >> 2)) & (P - 1), part = t & 3;
-  load_dwords<C::KW>(a.c.kc + (pk * P + ak) * (D / 2) + part * (D / 8), f.k);
-  constexpr int SB = D / 4 >= G ? D / 4 / G : 1;
-  const uint8_t* s = a.c.ks + (pk * P + ak) * (D / G) + part * (D / 4) / G;
-  if constexpr (SB == 4) f.ks = *(const uint32_t*)s;
-  else if constexpr (SB == 2) f.ks = *(const uint16_t*)s;
-  else f.ks = *s;
-  const int av = (int)(base + (t % C::TG) * C::TOK) & (P - 1);
+  // token of the page (the same for the wave when WIDE), and the lane's offset from it
+  const int64_t at = pk * P + (int)((WIDE ? base : base + (t >> 2)) & (P - 1));
+  const uint32_t row = WIDE ? t >> 2 : 0;
+  const uint8_t* kc = a.c.kc + at * (D / 2);
+#pragma unroll
+  for (int i = 0; i < C::KW; i += KB / 4) {
+    const auto w = KvLoad<KB, WIDE>::at(kc, row * (D / 2) + part * (D / 8) + i * 4, 0);
+#pragma unroll
+    for (int e = 0; e < KB / 4; e++) f.k[i + e] = w[e];
+  }
+  f.ks = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 4) / G, 0)[0];
+  const int tok = (t % C::TG) * C::TOK, av = (int)((WIDE ? base : base + tok) & (P - 1));
+  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + av;
+  const uint8_t* vs = a.c.vs + pv * (D / G) * P + av;
 #pragma unroll
   for (int r = 0; r < C::ROWS; r++) {
-    const int i = t / C::TG + r * (kThreads / C::TG);
-    load_dwords<C::VW>(a.c.vc + (pv * (D / 2) + i) * P + av, f.v[r]);
-    load_dwords<C::VW>(a.c.vs + (pv * (D / G) + 2 * i / G) * P + av, f.vs[r]);
+    const uint32_t i = t / C::TG + r * (kThreads / C::TG), off = WIDE ? tok : 0;
+    const auto w = KvLoad<VB, WIDE>::at(vc, (i << a.c.page_shift) + off, 0);
+    const auto s = KvLoad<VB, WIDE>::at(vs, ((2 * i / G) << a.c.page_shift) + off, 0);
+#pragma unroll
+    for (int e = 0; e < C::VW; e++) {
+      f.v[r][e] = w[e];
+      f.vs[r][e] = s[e];
+    }
   }
 }
 
@@ -161,7 +157,7 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-template <int MODE, int D>
+template <int MODE, int D, bool WIDE>
 __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(AttnArgs a) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f, kLag = MODE == 2 ? 8.0f : 3.0f;
   constexpr int QS = D / 16, NT = D / 32;
@@ -207,8 +203,8 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
 
   // queries: step s, slot j is channel 16 s + 8 hh + j
   u32x4_t q[QS];
-  const float qf = load_query<MODE, QS, 16>(
-      a, h, a.q + tok * a.qs + (int64_t)head * D + 8 * hh, q, half_max);
+  const ScoreScale sc = score_scale(
+      a, load_query<MODE, QS, 16>(a, h, a.q + tok * a.qs + (int64_t)head * D + 8 * hh, q, half_max));
 
   float m = -__builtin_inff(), l = 0.0f;
   f32x16_t o[NT];
@@ -216,29 +212,39 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
   for (int T = 0; T < NT; T++)
 #pragma unroll
     for (int r = 0; r < 16; r++) o[T][r] = 0.0f;
-  const float cap_in = a.cap > 0.0f ? 2.0f / a.cap : 0.0f, cap_out = a.cap * kLog2e;
   // row c of a key tile is the key that puts 8 consecutive ones into a lane's weights
   const int krow = (c & 16) | ((c & 4) << 1) | ((c & 8) >> 1) | (c & 3);
 
   auto compute = [&](int buf, int64_t base) {
+    // operands are read kAhead products early; the two key tiles alternate, so
+    // that a product never waits for the one before it
+    constexpr int kAhead = 4;
     f32x16_t s[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; kt++) {
+    for (int kt = 0; kt < 2; kt++)
 #pragma unroll
       for (int r = 0; r < 16; r++) s[kt][r] = 0.0f;
-#pragma unroll
-      for (int st = 0; st < QS; st++) {
-        const u32x4_t k = *(const u32x4_t*)(lds.k[buf] + (2 * st + hh) * L::KS + (32 * kt + krow) * 16);
-        s[kt] = mfma32<MODE>(k, q[st], s[kt]);
-      }
-    }
-    float f1 = qf;
+    auto key_at = [&](int i) {
+      return *(const u32x4_t*)(lds.k[buf] + (i & ~1) * L::KS + hh * L::KS + (32 * (i & 1) + krow) * 16);
+    };
+    u32x4_t ring[kAhead];
+    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = key_at(decltype(ii)::value); });
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<2 * QS>([&](auto ii) {
+      constexpr int i = decltype(ii)::value;
+      s[i & 1] = mfma32<MODE>(ring[i % kAhead], q[i >> 1], s[i & 1]);
+      if constexpr (i + kAhead < 2 * QS) ring[i % kAhead] = key_at(i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    auto value_at = [&](int i) {
+      return *(const u32x4_t*)(lds.v[buf] + (2 * (i / NT) + hh) * L::VS + (32 * (i % NT) + c) * 16);
+    };
+    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = value_at(decltype(ii)::value); });
     if (a.cap > 0.0f) {
-      f1 = 1.0f;
 #pragma unroll
       for (int kt = 0; kt < 2; kt++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) s[kt][r] = capped(s[kt][r] * qf, cap_in, cap_out);
+        for (int r = 0; r < 16; r++) s[kt][r] = capped(s[kt][r], sc.in);
     }
     const int4 ok = *(const int4*)lds.ok[buf];
     if (base < wlmax || base + 64 > whmin || !(ok.x & ok.y & ok.z & ok.w)) {
@@ -256,7 +262,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
     for (int kt = 0; kt < 2; kt++)
 #pragma unroll
       for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[kt][r]);
-    mx = fmaxf(m, half_max(mx) * f1);
+    mx = fmaxf(m, __builtin_fmaf(half_max(mx), sc.f, sc.off));
     if (__any(mx > m + kLag)) {
       const float fac = mx > m ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
       l *= fac;
@@ -266,14 +272,14 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
         for (int r = 0; r < 16; r++) o[T][r] *= fac;
       m = mx;
     }
-    const float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff;
+    const float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff - sc.off;
     u32x4_t p[4];
 #pragma unroll
     for (int kt = 0; kt < 2; kt++)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], f1, -ref));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r + 1], f1, -ref));
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], sc.f, -ref));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r + 1], sc.f, -ref));
         l += e0;
         l += e1;
         uint32_t w;
@@ -281,32 +287,32 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
         else w = bits_of(f16x2_t{(_Float16)e0, (_Float16)e1});
         p[2 * kt + (r >> 3)][(r & 7) >> 1] = w;
       }
-#pragma unroll
-    for (int s4 = 0; s4 < 4; s4++)
-#pragma unroll
-      for (int T = 0; T < NT; T++) {
-        const u32x4_t v = *(const u32x4_t*)(lds.v[buf] + (2 * s4 + hh) * L::VS + (32 * T + c) * 16);
-        o[T] = mfma32<MODE>(v, p[s4], o[T]);
-      }
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<4 * NT>([&](auto ii) {
+      constexpr int i = decltype(ii)::value;
+      o[i % NT] = mfma32<MODE>(ring[i % kAhead], p[i / NT], o[i % NT]);
+      if constexpr (i + kAhead < 4 * NT) ring[i % kAhead] = value_at(i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
   if (first < end) {
     auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
     TileCodes<MODE, D> f;
-    KvPages pg = tile_pages<MODE, D>(a, rt.b, base_of(first));
-    load_tile<MODE, D>(a, h, base_of(first), pg, f);
-    pg = tile_pages<MODE, D>(a, rt.b, base_of(first + 1));
+    KvPages pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first));
+    load_tile<MODE, D, WIDE>(a, h, base_of(first), pg, f);
+    pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first + 1));
     store_tile<MODE, D>(f, base_of(first), tlo, thi, lds, 0);
-    if (first + 1 < end) load_tile<MODE, D>(a, h, base_of(first + 1), pg, f);
-    pg = tile_pages<MODE, D>(a, rt.b, base_of(first + 2));
+    if (first + 1 < end) load_tile<MODE, D, WIDE>(a, h, base_of(first + 1), pg, f);
+    pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first + 2));
     for (uint32_t i = first; i < end; i++) {
       const int buf = (int)(i - first) & 1;
       __syncthreads();                   // tile i is decoded; the other buffer is free
       if (i + 1 < end) {
         store_tile<MODE, D>(f, base_of(i + 1), tlo, thi, lds, buf ^ 1);
         if (i + 2 < end) {
-          const KvPages next = tile_pages<MODE, D>(a, rt.b, base_of(i + 3));
-          load_tile<MODE, D>(a, h, base_of(i + 2), pg, f);
+          const KvPages next = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(i + 3));
+          load_tile<MODE, D, WIDE>(a, h, base_of(i + 2), pg, f);
           pg = next;
         }
       }
