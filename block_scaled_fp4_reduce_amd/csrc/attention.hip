@@ -294,9 +294,9 @@ int fp4_kv_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, uint16_t* o
   AttnArgs a;
   a.c = kv_view(c);
   a.q = x->q;
-  a.pt = x->page_table;
-  a.lens = x->kv_lens;
-  a.cu = x->cu_q;
+  a.pt = (const ConstInt*)x->page_table;
+  a.lens = (const ConstInt*)x->kv_lens;
+  a.cu = (const ConstInt*)x->cu_q;
   a.out = out;
   a.lse = lse;
   a.qs = x->q_stride;

@@ -31,10 +31,14 @@
 
 namespace fp4q {
 
+typedef __attribute__((address_space(4))) int32_t ConstInt;
+
 struct AttnArgs {
   KvView c;
   const uint16_t* q;
-  const int32_t *pt, *lens, *cu;
+  // constant address space: loads at wave-uniform places are scalar loads
+  // whatever the kernel has stored, and do not wait for the vector loads
+  const ConstInt *pt, *lens, *cu;
   uint16_t* out;
   float* lse;                            // [tokens][hq] or NULL
   float *po, *pm;                        // partials [splits][tokens][hq][D], [..][2] (max, sum)

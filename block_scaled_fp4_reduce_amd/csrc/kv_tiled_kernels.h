@@ -6,9 +6,11 @@
 // A workgroup of 4 waves takes 128 rows, 32 a wave (one column tile of the
 // 32x32x16 products).  Decoding a value costs about 1.3 vector instructions
 // and a row's softmax about 4 per key, so 128 rows per decoded value keep
-// the decode under a tenth of the softmax.  LDS holds two tiles; while one is
-// computed the next is decoded from registers into the other and the codes
-// after that are on their way from memory, with one barrier per 64 keys.
+// the decode at a third of the vector work.  That work and the matrix
+// products take about as long as each other, so they are woven together:
+// the next tile is decoded into LDS between the products of the scores, and
+// the second half of the tile's exponentials is taken between the products of
+// the first half's values (double buffers, one barrier per tile).
 //
 // LDS layout: 16-byte chunks, column after column, so that a wave's operand
 // reads are contiguous.  Keys: chunk (channels 8 x .. 8 x + 7, key).  Values:
@@ -38,61 +40,64 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
 // The codes of a thread's part of 64 tokens: D/4 channels of one key, and
 // TOK tokens of ROWS channel pairs.
 template <int MODE, int D>
-struct TileCodes {
+struct TileKeys {
   static constexpr int G = MODE == 2 ? 32 : 16;
-  static constexpr int KW = D / 32;                  // dwords of the key
+  static constexpr int W = D / 32;                   // dwords
+  uint32_t k[W], s;
+  int page;
+};
+template <int MODE, int D>
+struct TileValues {
+  static constexpr int G = MODE == 2 ? 32 : 16;
   static constexpr int TOK = D == 64 ? 8 : 16, TG = 64 / TOK;
   static constexpr int ROWS = D / 2 * TG / kThreads;
-  static constexpr int VW = TOK / 4;                 // dwords of a channel pair
-  uint32_t k[KW], ks;
-  uint32_t v[ROWS][VW], vs[ROWS][VW];
-  int kpage, vpage;
+  static constexpr int W = TOK / 4;                  // dwords of a channel pair
+  static constexpr int UNITS = ROWS * TOK / 8;       // pieces of 8 tokens of a pair
+  uint32_t v[ROWS][W], s[ROWS][W];
+  int page;
 };
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ KvPages tile_pages(const AttnArgs& a, uint32_t b, int64_t base) {
-  using C = TileCodes<MODE, D>;
-  const int t = (int)threadIdx.x;
-  KvPages p;
-  p.k = page_id(a, b, WIDE ? base : base + (t >> 2));
-  p.v = WIDE ? p.k : page_id(a, b, base + (t % C::TG) * C::TOK);
-  return p;
+__device__ __forceinline__ void load_tile_keys(const AttnArgs& a, int h, int64_t base, int page,
+                                               TileKeys<MODE, D>& f) {
+  using C = TileKeys<MODE, D>;
+  constexpr int G = C::G, B = C::W * 4 > 16 ? 16 : C::W * 4;
+  constexpr int SB = D / 4 >= G ? D / 4 / G : 1;
+  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, part = t & 3;
+  f.page = page;
+  // token of the page (the same for the wave when WIDE), and the lane's offset from it
+  const int64_t at = ((int64_t)(page < 0 ? 0 : page) * a.c.heads + h) * P +
+                     (int)((WIDE ? base : base + (t >> 2)) & (P - 1));
+  const uint32_t row = WIDE ? t >> 2 : 0;
+#pragma unroll
+  for (int i = 0; i < C::W; i += B / 4) {
+    const auto w = KvLoad<B, WIDE>::at(a.c.kc + at * (D / 2), row * (D / 2) + part * (D / 8) + i * 4, 0);
+#pragma unroll
+    for (int e = 0; e < B / 4; e++) f.k[i + e] = w[e];
+  }
+  f.s = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 4) / G, 0)[0];
 }
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int h, int64_t base, KvPages pg,
-                                          TileCodes<MODE, D>& f) {
-  using C = TileCodes<MODE, D>;
-  constexpr int G = C::G, KB = C::KW * 4 > 16 ? 16 : C::KW * 4, VB = C::VW * 4;
-  constexpr int SB = D / 4 >= G ? D / 4 / G : 1;
-  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, part = t & 3;
-  f.kpage = pg.k;
-  f.vpage = pg.v;
-  const int64_t pk = (int64_t)(pg.k < 0 ? 0 : pg.k) * a.c.heads + h;
-  const int64_t pv = (int64_t)(pg.v < 0 ? 0 : pg.v) * a.c.heads + h;
-  // token of the page (the same for the wave when WIDE), and the lane's offset from it
-  const int64_t at = pk * P + (int)((WIDE ? base : base + (t >> 2)) & (P - 1));
-  const uint32_t row = WIDE ? t >> 2 : 0;
-  const uint8_t* kc = a.c.kc + at * (D / 2);
-#pragma unroll
-  for (int i = 0; i < C::KW; i += KB / 4) {
-    const auto w = KvLoad<KB, WIDE>::at(kc, row * (D / 2) + part * (D / 8) + i * 4, 0);
-#pragma unroll
-    for (int e = 0; e < KB / 4; e++) f.k[i + e] = w[e];
-  }
-  f.ks = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 4) / G, 0)[0];
-  const int tok = (t % C::TG) * C::TOK, av = (int)((WIDE ? base : base + tok) & (P - 1));
-  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + av;
-  const uint8_t* vs = a.c.vs + pv * (D / G) * P + av;
+__device__ __forceinline__ void load_tile_values(const AttnArgs& a, int h, int64_t base, int page,
+                                                 TileValues<MODE, D>& f) {
+  using C = TileValues<MODE, D>;
+  constexpr int G = C::G, B = C::W * 4;
+  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, tok = (t % C::TG) * C::TOK;
+  f.page = page;
+  const int64_t pv = (int64_t)(page < 0 ? 0 : page) * a.c.heads + h;
+  const int at = (int)((WIDE ? base : base + tok) & (P - 1));
+  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + at;
+  const uint8_t* vs = a.c.vs + pv * (D / G) * P + at;
 #pragma unroll
   for (int r = 0; r < C::ROWS; r++) {
     const uint32_t i = t / C::TG + r * (kThreads / C::TG), off = WIDE ? tok : 0;
-    const auto w = KvLoad<VB, WIDE>::at(vc, (i << a.c.page_shift) + off, 0);
-    const auto s = KvLoad<VB, WIDE>::at(vs, ((2 * i / G) << a.c.page_shift) + off, 0);
+    const auto w = KvLoad<B, WIDE>::at(vc, (i << a.c.page_shift) + off, 0);
+    const auto s = KvLoad<B, WIDE>::at(vs, ((2 * i / G) << a.c.page_shift) + off, 0);
 #pragma unroll
-    for (int e = 0; e < C::VW; e++) {
+    for (int e = 0; e < C::W; e++) {
       f.v[r][e] = w[e];
-      f.vs[r][e] = s[e];
+      f.s[r][e] = s[e];
     }
   }
 }
@@ -105,47 +110,46 @@ struct TileLds {
   int ok[2][4];                          // the page of each 16 tokens is in the cache
 };
 
-// Decode into LDS; tokens outside [lo, hi) or without a page become zeros.
+// Unit U (one code dword) of a tile's keys into LDS.
+template <int U, int MODE, int D>
+__device__ __forceinline__ void store_key(const TileKeys<MODE, D>& f, TileLds<D>& lds, int buf) {
+  const int t = (int)threadIdx.x;
+  *(u32x4_t*)(lds.k[buf] + ((t & 3) * (D / 32) + U) * TileLds<D>::KS + (t >> 2) * 16) =
+      key_operand<MODE, U * 8 / TileKeys<MODE, D>::G>(f.k[U], f.s);
+}
+
+// Values of tokens outside [lo, hi) or without a page count as zeros: their
+// scales become zero.
 template <int MODE, int D>
-__device__ __forceinline__ void store_tile(const TileCodes<MODE, D>& f, int64_t base, int lo, int hi,
-                                           TileLds<D>& lds, int buf) {
-  using C = TileCodes<MODE, D>;
-  using L = TileLds<D>;
-  const int t = (int)threadIdx.x, part = t & 3, key = t >> 2;
-  static_for<C::KW>([&](auto dd) {
-    constexpr int d = decltype(dd)::value;
-    const u32x4_t w = key_operand<MODE, d * 8 / C::G>(f.k[d], f.ks);
-    *(u32x4_t*)(lds.k[buf] + (part * C::KW + d) * L::KS + key * 16) = w;
-  });
-  if ((t & 63) == 0) lds.ok[buf][t >> 6] = f.kpage >= 0;
-  const int tok = (t % C::TG) * C::TOK;
-  uint32_t keep[C::VW];
+__device__ __forceinline__ void drop_values(TileValues<MODE, D>& f, int64_t base, int lo, int hi) {
+  using C = TileValues<MODE, D>;
+  if (base >= lo && base + 64 <= hi && __all(f.page >= 0)) return;
+  const int tok = ((int)threadIdx.x % C::TG) * C::TOK;
 #pragma unroll
-  for (int w = 0; w < C::VW; w++) keep[w] = ~0u;
-  if (base < lo || base + 64 > hi || !__all(f.vpage >= 0)) {
+  for (int w = 0; w < C::W; w++) {
+    uint32_t keep = 0;
 #pragma unroll
-    for (int w = 0; w < C::VW; w++) {
-      keep[w] = 0;
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int j = (int)base + tok + 4 * w + r;
-        if (f.vpage >= 0 && j >= lo && j < hi) keep[w] |= 255u << (8 * r);
-      }
+    for (int r = 0; r < 4; r++) {
+      const int64_t j = base + tok + 4 * w + r;
+      if (f.page >= 0 && j >= lo && j < hi) keep |= 255u << (8 * r);
     }
-  }
 #pragma unroll
-  for (int r = 0; r < C::ROWS; r++) {
-    const int i = t / C::TG + r * (kThreads / C::TG);
-#pragma unroll
-    for (int y = 0; y < C::TOK / 8; y++) {
-      u32x4_t even, odd;
-      value_operands<MODE>(f.v[r][2 * y], f.v[r][2 * y + 1], f.vs[r][2 * y] & keep[2 * y],
-                           f.vs[r][2 * y + 1] & keep[2 * y + 1], even, odd);
-      uint8_t* o = lds.v[buf] + (tok / 8 + y) * L::VS + i * 16;
-      *(u32x4_t*)o = even;
-      *(u32x4_t*)(o + D / 2 * 16) = odd;
-    }
+    for (int r = 0; r < C::ROWS; r++) f.s[r][w] &= keep;
   }
+}
+
+// Unit U (8 tokens of a channel pair) of a tile's values into LDS.
+template <int U, int MODE, int D>
+__device__ __forceinline__ void store_value(const TileValues<MODE, D>& f, TileLds<D>& lds, int buf) {
+  using C = TileValues<MODE, D>;
+  constexpr int Y = C::TOK / 8, r = U / Y, y = U % Y;
+  const int t = (int)threadIdx.x;
+  u32x4_t even, odd;
+  value_operands<MODE>(f.v[r][2 * y], f.v[r][2 * y + 1], f.s[r][2 * y], f.s[r][2 * y + 1], even, odd);
+  uint8_t* o = lds.v[buf] + ((t % C::TG) * Y + y) * TileLds<D>::VS +
+               (t / C::TG + r * (kThreads / C::TG)) * 16;
+  *(u32x4_t*)o = even;
+  *(u32x4_t*)(o + D / 2 * 16) = odd;
 }
 
 __device__ __forceinline__ float half_max(float v) {
@@ -192,9 +196,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
     if (empty) return;
   }
   const uint32_t w0 = rt.row0 + 32 * wave;
-  const bool alive = w0 < rt.rows;
-  const int whmin = hi_of(end_of(w0)), whmax = alive ? hi_of(end_of(w0 + 31)) : 0;
-  const int wlmin = lo_of(whmin), wlmax = lo_of(whmax);
+  const int whmin = hi_of(end_of(w0)), wlmax = lo_of(hi_of(end_of(w0 + 31)));
   const bool live = w0 + c < rt.rows;
   const uint32_t row = end_of(w0 + c);   // columns past the last row repeat it, unstored
   const int64_t tok = rt.tok0 + row / group;
@@ -215,38 +217,52 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
   // row c of a key tile is the key that puts 8 consecutive ones into a lane's weights
   const int krow = (c & 16) | ((c & 4) << 1) | ((c & 8) >> 1) | (c & 3);
 
-  auto compute = [&](int buf, int64_t base) {
-    // operands are read kAhead products early; the two key tiles alternate, so
-    // that a product never waits for the one before it
-    constexpr int kAhead = 4;
+  constexpr int kAhead = D == 256 ? 3 : 4;   // operands are read this many products early
+  using TK = TileKeys<MODE, D>;
+  using TV = TileValues<MODE, D>;
+  auto key_at = [&](int buf, int i) {
+    return *(const u32x4_t*)(lds.k[buf] + (2 * (i % QS) + hh) * L::KS + (32 * (i / QS) + krow) * 16);
+  };
+  auto value_at = [&](int buf, int i) {
+    return *(const u32x4_t*)(lds.v[buf] + (2 * (i / NT) + hh) * L::VS + (32 * (i % NT) + c) * 16);
+  };
+  const bool alive = w0 < rt.rows;       // a wave without rows only decodes
+  TK kf;
+  TV vf;
+  constexpr int UNITS = TK::W + TV::UNITS;
+  auto store = [&](auto uu, int buf) {   // unit u of the decode
+    constexpr int u = decltype(uu)::value;
+    if constexpr (u < TK::W) store_key<u>(kf, lds, buf);
+    else store_value<u - TK::W>(vf, lds, buf);
+  };
+
+  // one tile: its scores while the next is decoded, its weights, its values
+  auto tile = [&](int buf, int64_t base) {
     f32x16_t s[2];
-#pragma unroll
-    for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) s[kt][r] = 0.0f;
-    auto key_at = [&](int i) {
-      return *(const u32x4_t*)(lds.k[buf] + (i & ~1) * L::KS + hh * L::KS + (32 * (i & 1) + krow) * 16);
-    };
     u32x4_t ring[kAhead];
-    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = key_at(decltype(ii)::value); });
+    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = key_at(buf, decltype(ii)::value); });
     __builtin_amdgcn_sched_barrier(0);
     static_for<2 * QS>([&](auto ii) {
-      constexpr int i = decltype(ii)::value;
-      s[i & 1] = mfma32<MODE>(ring[i % kAhead], q[i >> 1], s[i & 1]);
-      if constexpr (i + kAhead < 2 * QS) ring[i % kAhead] = key_at(i + kAhead);
+      constexpr int i = decltype(ii)::value, u0 = i * UNITS / (2 * QS), u1 = (i + 1) * UNITS / (2 * QS);
+      if constexpr (i % QS == 0) {
+#pragma unroll
+        for (int r = 0; r < 16; r++) s[i / QS][r] = 0.0f;
+      }
+      s[i / QS] = mfma32<MODE>(ring[i % kAhead], q[i % QS], s[i / QS]);
+      if constexpr (i + kAhead < 2 * QS) ring[i % kAhead] = key_at(buf, i + kAhead);
+      static_for<u1 - u0>([&](auto kk) {
+        store(std::integral_constant<int, u0 + decltype(kk)::value>{}, buf ^ 1);
+      });
       __builtin_amdgcn_sched_barrier(0);
     });
-    auto value_at = [&](int i) {
-      return *(const u32x4_t*)(lds.v[buf] + (2 * (i / NT) + hh) * L::VS + (32 * (i % NT) + c) * 16);
-    };
-    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = value_at(decltype(ii)::value); });
+    const int4 ok = *(const int4*)lds.ok[buf];
+    static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = value_at(buf, decltype(ii)::value); });
     if (a.cap > 0.0f) {
 #pragma unroll
       for (int kt = 0; kt < 2; kt++)
 #pragma unroll
         for (int r = 0; r < 16; r++) s[kt][r] = capped(s[kt][r], sc.in);
     }
-    const int4 ok = *(const int4*)lds.ok[buf];
     if (base < wlmax || base + 64 > whmin || !(ok.x & ok.y & ok.z & ok.w)) {
       const int oks[4] = {ok.x, ok.y, ok.z, ok.w};
 #pragma unroll
@@ -273,51 +289,83 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
       m = mx;
     }
     const float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff - sc.off;
+    // weights two at a time (pair j); a pair's arguments, exponentials and sum
+    // are taken in three successive places
     u32x4_t p[4];
-#pragma unroll
-    for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], sc.f, -ref));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r + 1], sc.f, -ref));
-        l += e0;
-        l += e1;
-        uint32_t w;
-        if constexpr (MODE == 2) w = bf16x2_of(e0, e1);
-        else w = bits_of(f16x2_t{(_Float16)e0, (_Float16)e1});
-        p[2 * kt + (r >> 3)][(r & 7) >> 1] = w;
-      }
+    float x0, x1, e0 = 0.0f, e1 = 0.0f;
+    auto args = [&](auto jj) {
+      constexpr int r = 2 * decltype(jj)::value;
+      x0 = __builtin_fmaf(s[r >> 4][r & 15], sc.f, -ref);
+      x1 = __builtin_fmaf(s[r >> 4][(r & 15) + 1], sc.f, -ref);
+    };
+    auto pack = [&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      l += e0;
+      l += e1;
+      uint32_t w;
+      if constexpr (MODE == 2) w = bf16x2_of(e0, e1);
+      else w = bits_of(f16x2_t{(_Float16)e0, (_Float16)e1});
+      p[j >> 2][j & 3] = w;
+    };
+    auto weight = [&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      if constexpr (j % 8 > 0) pack(std::integral_constant<int, j - 1>{});
+      e0 = __builtin_amdgcn_exp2f(x0);
+      e1 = __builtin_amdgcn_exp2f(x1);
+      if constexpr (j % 8 < 7) args(std::integral_constant<int, j + 1>{});
+    };
+    args(std::integral_constant<int, 0>{});
+    static_for<8>(weight);
+    pack(std::integral_constant<int, 7>{});
+    args(std::integral_constant<int, 8>{});
     __builtin_amdgcn_sched_barrier(0);
-    static_for<4 * NT>([&](auto ii) {
-      constexpr int i = decltype(ii)::value;
+    constexpr int N = 4 * NT;
+    static_for<N>([&](auto ii) {
+      constexpr int i = decltype(ii)::value, w0 = i * 16 / N, w1 = (i + 1) * 16 / N;
       o[i % NT] = mfma32<MODE>(ring[i % kAhead], p[i / NT], o[i % NT]);
-      if constexpr (i + kAhead < 4 * NT) ring[i % kAhead] = value_at(i + kAhead);
+      if constexpr (i + kAhead < N) ring[i % kAhead] = value_at(buf, i + kAhead);
+      if constexpr (i < N / 2) {
+        static_for<w1 - w0>([&](auto kk) { weight(std::integral_constant<int, 8 + w0 + decltype(kk)::value>{}); });
+        if constexpr (i == N / 2 - 1) pack(std::integral_constant<int, 15>{});
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
   };
 
+  // Tiles past the end are decoded too (from page 0 where there is none), which
+  // keeps the loop free of cases; nothing uses them.
   if (first < end) {
-    auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
-    TileCodes<MODE, D> f;
-    KvPages pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first));
-    load_tile<MODE, D, WIDE>(a, h, base_of(first), pg, f);
-    pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first + 1));
-    store_tile<MODE, D>(f, base_of(first), tlo, thi, lds, 0);
-    if (first + 1 < end) load_tile<MODE, D, WIDE>(a, h, base_of(first + 1), pg, f);
-    pg = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(first + 2));
-    for (uint32_t i = first; i < end; i++) {
-      const int buf = (int)(i - first) & 1;
-      __syncthreads();                   // tile i is decoded; the other buffer is free
-      if (i + 1 < end) {
-        store_tile<MODE, D>(f, base_of(i + 1), tlo, thi, lds, buf ^ 1);
-        if (i + 2 < end) {
-          const KvPages next = tile_pages<MODE, D, WIDE>(a, rt.b, base_of(i + 3));
-          load_tile<MODE, D, WIDE>(a, h, base_of(i + 2), pg, f);
-          pg = next;
-        }
-      }
-      const int64_t base = base_of(i);
-      if (base < whmax && base + kAttnKeys > wlmin) compute(buf, base);
+    const uint32_t count = end - first;
+    auto base_of = [&](uint32_t i) { return base0 + (int64_t)(first + i) * kAttnKeys; };
+    auto key_page = [&](uint32_t i) {
+      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x >> 2));
+    };
+    auto value_page = [&](uint32_t i) {
+      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x % TV::TG * TV::TOK));
+    };
+    auto load = [&](uint32_t i, int kp, int vp) {
+      load_tile_keys<MODE, D, WIDE>(a, h, base_of(i), kp, kf);
+      load_tile_values<MODE, D, WIDE>(a, h, base_of(i), vp, vf);
+    };
+    auto ready = [&](uint32_t i) {       // what the decode of tile i needs once
+      drop_values(vf, base_of(i), tlo, thi);
+      if (lane == 0) lds.ok[i & 1][wave] = kf.page >= 0;
+    };
+    auto store_all = [&](int buf) { static_for<UNITS>([&](auto u) { store(u, buf); }); };
+    load(0, key_page(0), value_page(0));
+    int kp = key_page(1), vp = value_page(1);
+    ready(0);
+    store_all(0);
+    load(1, kp, vp);
+    for (uint32_t i = 0; i < count; i++) {
+      const int buf = (int)i & 1;
+      kp = key_page(i + 2);
+      vp = value_page(i + 2);
+      __syncthreads();                   // tile i is decoded, the other buffer free
+      ready(i + 1);
+      if (alive) tile(buf, base_of(i));
+      else store_all(buf ^ 1);
+      load(i + 2, kp, vp);
     }
   }
 
