@@ -168,8 +168,13 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   const int64_t blocks = cdiv(keys, kAttnKeys);
   // Workgroups wanted per kv head.  How they are shared out among the
   // sequences depends on lengths that only the device knows (item_of); a
-  // tile gets at most four times an even share.
-  const int per_cu = p.nt == 0 ? 4 : (p.nt == 2 || c->head_dim == 256 ? 2 : 3);
+  // tile gets at most four times an even share.  As many as run at once (by
+  // their registers), so that all of them end together: chunks of 512 tokens
+  // over 6144 cached, 3 to a CU: 171 us, 2: 209, 4: 203, 6: 200.
+  const bool wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
+  const int d = c->head_dim;
+  const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + wide : 1))
+                               : (p.nt == 2 || d == 256 ? 2 : (d == 128 ? 3 : 4));
   p.want = cdiv(per_cu * (int64_t)num_cus(), c->heads);
   const int64_t share = cdiv(4 * p.want, p.tiles), room = cdiv(blocks, 4);
   p.splits = p.tiles >= p.want ? 1 : (share < room ? share : room);
@@ -188,7 +193,8 @@ size_t attention_ws(const fp4_kv_cache* c, const fp4_kv_queries* x, const AttnPl
 template <int MODE, int D>
 hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)(p.places * a.c.heads);
-  const bool wide = a.c.page_shift >= 6;   // a block of 64 keys lies in one page
+  // a block of keys lies in one page
+  const bool wide = (1 << a.c.page_shift) >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
     e = wide ? launch(kv_tiled_kernel<MODE, D, true>, grid, kThreads, st, a)
@@ -209,7 +215,7 @@ hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st
     while (groups < most && groups * 4 < p.splits) groups *= 2;
     e = first(e, launch(kv_attention_join_kernel<MODE, D>,
                         (unsigned)cdiv(a.tokens * a.hq, kThreads / (lanes * groups)), kThreads, st,
-                        a, groups));
+                        a, groups, a.tokens * a.hq <= 4096));
   }
   return e;
 }

@@ -773,7 +773,7 @@ void kv_attention_kernel(AttnArgs a) {
 // `groups` (a power of two) for a query row, the groups taking its parts in
 // turn.
 template <int MODE, int D>
-__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int groups) {
+__global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a, int groups, bool eager) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f;
   constexpr int L = D / 4;
   __shared__ float4 sx[kThreads];
@@ -795,13 +795,22 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
     top = mm;
   };
   if (live) {
-    const int n = a.parts[row];
-#pragma unroll 4
-    for (int s = grp; s < n; s += groups) {
-      const float2 ml = *(const float2*)(a.pm + (s * rows + row) * 2);
-      float4 y = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
-      if (ml.y == 0.0f) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // its sums were not written
-      add(ml.x, ml.y, y);
+    // with few rows the loads do not wait for the number of parts (sums that
+    // were not written are read and dropped): the call is all latency
+    const int n = a.parts[row], most = eager ? a.splits : n;
+    for (int s0 = grp; s0 < most; s0 += 4 * groups) {
+      float2 ml[4];
+      float4 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const int64_t s = min(s0 + e * groups, most - 1);
+        ml[e] = *(const float2*)(a.pm + (s * rows + row) * 2);
+        y[e] = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
+      }
+      if (s0 >= n) break;
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (s0 + e * groups < n && ml[e].y != 0.0f) add(ml[e].x, ml[e].y, y[e]);
     }
   }
   if (groups > 1) {

@@ -103,29 +103,42 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvView c, const uint
   __shared__ __align__(16) uint8_t codes[D / 2 * LD], scales[GPH * LD];
   const int h = (int)(blockIdx.x % (uint32_t)c.heads);
   const int64_t t0 = (int64_t)(blockIdx.x / (uint32_t)c.heads) * TT;
-  load_slots<TT>(c, slots, t0, tokens, sl);
-  const int P = 1 << c.page_shift, live = (int)(tokens - t0 < TT ? tokens - t0 : TT);
-  const TensorScale kts = tensor_scale(MODE == 2 ? 0.0f : c.kam[h], MODE == 1);
-  const TensorScale vts = tensor_scale(MODE == 2 ? 0.0f : c.vam[h], MODE == 1);
-  // values first (the smaller half of the items), then keys
+  const int live = (int)(tokens - t0 < TT ? tokens - t0 : TT);
+  // all inputs are on their way before the slots are looked at
+  constexpr int ITEMS = (2 * TT * GPH + kThreads - 1) / kThreads;
+  uint4 x[ITEMS][G / 8];
 #pragma unroll
-  for (int it = (int)threadIdx.x; it < 2 * TT * GPH; it += kThreads) {
+  for (int i = 0; i < ITEMS; i++) {
+    const int it = (int)threadIdx.x + i * kThreads;
+    const bool isv = it < TT * GPH;      // values first, then keys
+    const int r = isv ? it : it - TT * GPH, tok = r / GPH, g = r % GPH;
+    if (it >= 2 * TT * GPH || tok >= live) continue;
+    const uint4* from = (const uint4*)((isv ? v + (t0 + tok) * vs : k + (t0 + tok) * ks) + h * D + g * G);
+#pragma unroll
+    for (int e = 0; e < G / 8; e++) x[i][e] = from[e];
+  }
+  const float kam = MODE == 2 ? 0.0f : c.kam[h], vam = MODE == 2 ? 0.0f : c.vam[h];
+  load_slots<TT>(c, slots, t0, tokens, sl);
+  const int P = 1 << c.page_shift;
+  const TensorScale kts = tensor_scale(kam, MODE == 1), vts = tensor_scale(vam, MODE == 1);
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) {
+    const int it = (int)threadIdx.x + i * kThreads;
     const bool isv = it < TT * GPH;
     const int r = isv ? it : it - TT * GPH, tok = r / GPH, g = r % GPH;
-    if (tok >= live) continue;
+    if (it >= 2 * TT * GPH || tok >= live) continue;
     const int64_t slot = sl.slot[tok], page = slot_page(c, slot);
     if (page < 0) continue;
-    const uint4* x = (const uint4*)((isv ? v + (t0 + tok) * vs : k + (t0 + tok) * ks) + h * D + g * G);
     float y[G];
 #pragma unroll
-    for (int j = 0; j < G / 8; j++) unpack8(x[j], y + 8 * j);
+    for (int e = 0; e < G / 8; e++) unpack8(x[i][e], y + 8 * e);
     uint32_t w[G / 8], scale;
     if constexpr (MODE == 2) kv_quant32(y, w, scale);
     else kv_quant16<MODE == 1>(y, isv ? vts : kts, w[0], w[1], scale);
     if (isv) {
 #pragma unroll
-      for (int j = 0; j < G / 2; j++)
-        codes[(g * (G / 2) + j) * LD + tok] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+      for (int e = 0; e < G / 2; e++)
+        codes[(g * (G / 2) + e) * LD + tok] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
       scales[g * LD + tok] = (uint8_t)scale;
     } else {
       const int64_t at = (page * c.heads + h) * P + (slot & (P - 1));
@@ -186,45 +199,62 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvView c, const int64
   const int P = 1 << c.page_shift, live = (int)(tokens - t0 < TT ? tokens - t0 : TT);
   const float ka = MODE == 2 ? 1.0f : tensor_scale(c.kam[h], MODE == 1).alpha;
   const float va = MODE == 2 ? 1.0f : tensor_scale(c.vam[h], MODE == 1).alpha;
+  // every load of the codes goes out before the first store
+  constexpr int VI = (D / 2 * (TT / 16) + kThreads - 1) / kThreads, KI = TT * (D / 8) / kThreads;
+  constexpr int KITEMS = KI ? KI : 1;
+  uint32_t vw[VI][4], vsc[VI][4], kw[KITEMS], ksc[KITEMS];
 #pragma unroll
-  for (int it = (int)threadIdx.x; it < D / 2 * (TT / 16); it += kThreads) {
+  for (int i = 0; i < VI; i++) {
+    const int it = (int)threadIdx.x + i * kThreads;
     const int seg = it % (TT / 16), row = it / (TT / 16), g = 2 * row / G;
-    uint32_t w[4] = {}, s[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; e++) vw[i][e] = vsc[i][e] = 0;
+    if (it >= D / 2 * (TT / 16)) continue;
     if (sl.runs >> seg & 1) {
       const int64_t slot = sl.slot[seg * 16], ph = (slot >> c.page_shift) * c.heads + h;
       const uint4 a = *(const uint4*)(c.vc + (ph * (D / 2) + row) * P + (slot & (P - 1)));
       const uint4 b = *(const uint4*)(c.vs + (ph * GPH + g) * P + (slot & (P - 1)));
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
+      vw[i][0] = a.x; vw[i][1] = a.y; vw[i][2] = a.z; vw[i][3] = a.w;
+      vsc[i][0] = b.x; vsc[i][1] = b.y; vsc[i][2] = b.z; vsc[i][3] = b.w;
     } else {
 #pragma unroll
       for (int e = 0; e < 16; e++) {
         const int64_t slot = sl.slot[seg * 16 + e], page = slot_page(c, slot);
         if (page < 0) continue;
         const int64_t ph = page * c.heads + h;
-        w[e / 4] |= (uint32_t)c.vc[(ph * (D / 2) + row) * P + (slot & (P - 1))] << (8 * (e % 4));
-        s[e / 4] |= (uint32_t)c.vs[(ph * GPH + g) * P + (slot & (P - 1))] << (8 * (e % 4));
+        vw[i][e / 4] |= (uint32_t)c.vc[(ph * (D / 2) + row) * P + (slot & (P - 1))] << (8 * (e % 4));
+        vsc[i][e / 4] |= (uint32_t)c.vs[(ph * GPH + g) * P + (slot & (P - 1))] << (8 * (e % 4));
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < KITEMS; i++) {
+    const int it = (int)threadIdx.x + i * kThreads, tok = it / (D / 8), ch = it % (D / 8) * 8;
+    kw[i] = ksc[i] = 0;
+    if (tok >= live) continue;
+    const int64_t slot = sl.slot[tok], page = slot_page(c, slot);
+    if (page >= 0) {
+      const int64_t at = (page * c.heads + h) * P + (slot & (P - 1));
+      kw[i] = *(const uint32_t*)(c.kc + at * (D / 2) + ch / 2);
+      ksc[i] = c.ks[at * GPH + ch / G];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VI; i++) {
+    const int it = (int)threadIdx.x + i * kThreads, seg = it % (TT / 16), row = it / (TT / 16);
+    if (it >= D / 2 * (TT / 16)) continue;
     static_for<16>([&](auto ee) {
       constexpr int e = decltype(ee)::value;
-      const float2_t x = fp4x2_to_f32<e % 4>(w[e / 4], 1.0f);
-      const float f = kv_scale<MODE>((s[e / 4] >> (8 * (e % 4))) & 255u, va);
+      const float2_t x = fp4x2_to_f32<e % 4>(vw[i][e / 4], 1.0f);
+      const float f = kv_scale<MODE>((vsc[i][e / 4] >> (8 * (e % 4))) & 255u, va);
       turned[(seg * 16 + e) * LD + row] = bf16x2_of(x.x * f, x.y * f);
     });
   }
 #pragma unroll
-  for (int it = (int)threadIdx.x; it < TT * (D / 8); it += kThreads) {
-    const int tok = it / (D / 8), ch = it % (D / 8) * 8;
+  for (int i = 0; i < KITEMS; i++) {
+    const int it = (int)threadIdx.x + i * kThreads, tok = it / (D / 8), ch = it % (D / 8) * 8;
     if (tok >= live) continue;
-    const int64_t slot = sl.slot[tok], page = slot_page(c, slot);
-    uint32_t w = 0, s = 0;
-    if (page >= 0) {
-      const int64_t at = (page * c.heads + h) * P + (slot & (P - 1));
-      w = *(const uint32_t*)(c.kc + at * (D / 2) + ch / 2);
-      s = c.ks[at * GPH + ch / G];
-    }
-    *(uint4*)(k + (t0 + tok) * ks + h * D + ch) = kv_decode8(w, kv_scale<MODE>(s, ka));
+    *(uint4*)(k + (t0 + tok) * ks + h * D + ch) = kv_decode8(kw[i], kv_scale<MODE>(ksc[i], ka));
   }
   __syncthreads();
 #pragma unroll

@@ -1,21 +1,29 @@
 // kv_tiled_kernels.h -- attention over the paged FP4 cache for many query
 // rows per kv head (prompts, chunks): the mathematics of
-// kv_attention_kernels.h, with the decoded keys and values of 64 tokens
+// kv_attention_kernels.h, with the decoded keys and values of 32 tokens
 // shared through LDS.
 //
 // A workgroup of 4 waves takes 128 rows, 32 a wave (one column tile of the
 // 32x32x16 products).  Decoding a value costs about 1.3 vector instructions
-// and a row's softmax about 4 per key, so 128 rows per decoded value keep
-// the decode at a third of the vector work.  That work and the matrix
-// products take about as long as each other, so they are woven together:
-// the next tile is decoded into LDS between the products of the scores, and
-// the second half of the tile's exponentials is taken between the products of
-// the first half's values (double buffers, one barrier per tile).
+// and a row's softmax about 4 per key (12 with capped scores), so 128 rows per
+// decoded value keep the decode at a third of the vector work.  That work and
+// the matrix products take about as long as each other, so they are woven
+// together: the next tile is decoded into LDS between the products of the
+// scores, and the second half of the tile's exponentials is taken between the
+// products of the first half's values (double buffers, one barrier per tile).
+// Tiles of 32 keys keep the registers of a wave at 168, so that three run on
+// a SIMD.  Vector instructions bound it: counted at D = 128, MXFP4, capped,
+// they issue in 67% of the cycles and the matrix unit runs in 33%.
+//
+// Measured, D = 128, 32 query and 8 kv heads: a prompt of 8192 tokens, window
+// 4096, capped, MXFP4: 521 us (790 TFLOP/s of the products); 4 sequences with
+// up to 512 new tokens over 6144, NVFP4 4/6: 158 us with the join (632
+// TFLOP/s).  Tiles of 64 keys and two waves a SIMD: 522 and 169 us.
 //
 // LDS layout: 16-byte chunks, column after column, so that a wave's operand
 // reads are contiguous.  Keys: chunk (channels 8 x .. 8 x + 7, key).  Values:
 // chunk (tokens 8 y .. 8 y + 7, channel), even channels before odd ones.  The
-// padding of a column (16 and 32 bytes) spreads the decoding lanes' stores
+// padding of a column (16 and 64 bytes) spreads the decoding lanes' stores
 // over all banks.
 #pragma once
 
@@ -24,6 +32,7 @@
 namespace fp4q {
 
 constexpr int kTileRows = 128;           // query rows of a workgroup
+constexpr int kTileKeys = 32;            // keys of a tile
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
@@ -37,93 +46,61 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// The codes of a thread's part of 64 tokens: D/4 channels of one key, and
-// TOK tokens of ROWS channel pairs.
+// The codes of a thread's part of a tile: D/8 channels of one key, and TOK
+// tokens of one channel pair.
 template <int MODE, int D>
-struct TileKeys {
+struct TileCodes {
   static constexpr int G = MODE == 2 ? 32 : 16;
-  static constexpr int W = D / 32;                   // dwords
-  uint32_t k[W], s;
-  int page;
-};
-template <int MODE, int D>
-struct TileValues {
-  static constexpr int G = MODE == 2 ? 32 : 16;
-  static constexpr int TOK = D == 64 ? 8 : 16, TG = 64 / TOK;
-  static constexpr int ROWS = D / 2 * TG / kThreads;
-  static constexpr int W = TOK / 4;                  // dwords of a channel pair
-  static constexpr int UNITS = ROWS * TOK / 8;       // pieces of 8 tokens of a pair
-  uint32_t v[ROWS][W], s[ROWS][W];
-  int page;
+  static constexpr int B = D / 16, W = D / 64;       // bytes and dwords of either
+  static constexpr int TOK = B, TG = kTileKeys / TOK;
+  static constexpr int VU = D == 64 ? 1 : W / 2;     // pieces of 8 tokens (D = 64: half of one)
+  static constexpr int UNITS = W + VU;
+  uint32_t k[W], ks, v[W], vs[W];
+  int kpage, vpage;
 };
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_tile_keys(const AttnArgs& a, int h, int64_t base, int page,
-                                               TileKeys<MODE, D>& f) {
-  using C = TileKeys<MODE, D>;
-  constexpr int G = C::G, B = C::W * 4 > 16 ? 16 : C::W * 4;
-  constexpr int SB = D / 4 >= G ? D / 4 / G : 1;
-  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, part = t & 3;
-  f.page = page;
-  // token of the page (the same for the wave when WIDE), and the lane's offset from it
-  const int64_t at = ((int64_t)(page < 0 ? 0 : page) * a.c.heads + h) * P +
-                     (int)((WIDE ? base : base + (t >> 2)) & (P - 1));
-  const uint32_t row = WIDE ? t >> 2 : 0;
+__device__ __forceinline__ void load_tile(const AttnArgs& a, int h, int64_t base, int kpage,
+                                          int vpage, TileCodes<MODE, D>& f) {
+  using C = TileCodes<MODE, D>;
+  constexpr int G = C::G, SB = D / 8 >= G ? D / 8 / G : 1;
+  const int t = (int)threadIdx.x, shift = a.c.page_shift, P = 1 << shift, part = t & 7;
+  f.kpage = kpage;
+  f.vpage = vpage;
+  // page and token of it (the same for the wave when WIDE), and the lane's offset
+  const int64_t pk = (int64_t)(kpage < 0 ? 0 : kpage) * a.c.heads + h;
+  const int64_t at = (pk << shift) + (int)((WIDE ? base : base + (t >> 3)) & (P - 1));
+  const uint32_t row = WIDE ? t >> 3 : 0;
+  const auto k = KvLoad<C::B, WIDE>::at(a.c.kc + at * (D / 2), row * (D / 2) + part * C::B, 0);
+  f.ks = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 8) / G, 0)[0];
+  const int64_t pv = WIDE ? pk : (int64_t)(vpage < 0 ? 0 : vpage) * a.c.heads + h;
+  const int tok = (t % C::TG) * C::TOK, av = (int)((WIDE ? base : base + tok) & (P - 1));
+  const uint32_t i = t / C::TG, off = WIDE ? tok : 0;
+  const auto v = KvLoad<C::B, WIDE>::at(a.c.vc + ((pv * (D / 2)) << shift) + av, (i << shift) + off, 0);
+  const auto s = KvLoad<C::B, WIDE>::at(a.c.vs + ((pv * (D / G)) << shift) + av,
+                                        ((2 * i / G) << shift) + off, 0);
 #pragma unroll
-  for (int i = 0; i < C::W; i += B / 4) {
-    const auto w = KvLoad<B, WIDE>::at(a.c.kc + at * (D / 2), row * (D / 2) + part * (D / 8) + i * 4, 0);
-#pragma unroll
-    for (int e = 0; e < B / 4; e++) f.k[i + e] = w[e];
-  }
-  f.s = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 4) / G, 0)[0];
-}
-
-template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_tile_values(const AttnArgs& a, int h, int64_t base, int page,
-                                                 TileValues<MODE, D>& f) {
-  using C = TileValues<MODE, D>;
-  constexpr int G = C::G, B = C::W * 4;
-  const int t = (int)threadIdx.x, P = 1 << a.c.page_shift, tok = (t % C::TG) * C::TOK;
-  f.page = page;
-  const int64_t pv = (int64_t)(page < 0 ? 0 : page) * a.c.heads + h;
-  const int at = (int)((WIDE ? base : base + tok) & (P - 1));
-  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + at;
-  const uint8_t* vs = a.c.vs + pv * (D / G) * P + at;
-#pragma unroll
-  for (int r = 0; r < C::ROWS; r++) {
-    const uint32_t i = t / C::TG + r * (kThreads / C::TG), off = WIDE ? tok : 0;
-    const auto w = KvLoad<B, WIDE>::at(vc, (i << a.c.page_shift) + off, 0);
-    const auto s = KvLoad<B, WIDE>::at(vs, ((2 * i / G) << a.c.page_shift) + off, 0);
-#pragma unroll
-    for (int e = 0; e < C::W; e++) {
-      f.v[r][e] = w[e];
-      f.s[r][e] = s[e];
-    }
+  for (int e = 0; e < C::W; e++) {
+    f.k[e] = k[e];
+    f.v[e] = v[e];
+    f.vs[e] = s[e];
   }
 }
 
 template <int D>
 struct TileLds {
-  static constexpr int KS = 64 * 16 + 16, VS = D * 16 + 32;      // bytes of a column
-  static constexpr int K = D / 8 * KS, V = 8 * VS;
+  static constexpr int KS = kTileKeys * 16 + 16, VS = D * 16 + 64;      // bytes of a column
+  static constexpr int K = D / 8 * KS, V = kTileKeys / 8 * VS;
   uint8_t k[2][K], v[2][V];
-  int ok[2][4];                          // the page of each 16 tokens is in the cache
+  int ok[2][2];                          // the page of each 16 tokens is in the cache
 };
-
-// Unit U (one code dword) of a tile's keys into LDS.
-template <int U, int MODE, int D>
-__device__ __forceinline__ void store_key(const TileKeys<MODE, D>& f, TileLds<D>& lds, int buf) {
-  const int t = (int)threadIdx.x;
-  *(u32x4_t*)(lds.k[buf] + ((t & 3) * (D / 32) + U) * TileLds<D>::KS + (t >> 2) * 16) =
-      key_operand<MODE, U * 8 / TileKeys<MODE, D>::G>(f.k[U], f.s);
-}
 
 // Values of tokens outside [lo, hi) or without a page count as zeros: their
 // scales become zero.
 template <int MODE, int D>
-__device__ __forceinline__ void drop_values(TileValues<MODE, D>& f, int64_t base, int lo, int hi) {
-  using C = TileValues<MODE, D>;
-  if (base >= lo && base + 64 <= hi && __all(f.page >= 0)) return;
+__device__ __forceinline__ void drop_values(TileCodes<MODE, D>& f, int64_t base, int lo, int hi) {
+  using C = TileCodes<MODE, D>;
+  if (base >= lo && base + kTileKeys <= hi && __all(f.vpage >= 0)) return;
   const int tok = ((int)threadIdx.x % C::TG) * C::TOK;
 #pragma unroll
   for (int w = 0; w < C::W; w++) {
@@ -131,25 +108,36 @@ __device__ __forceinline__ void drop_values(TileValues<MODE, D>& f, int64_t base
 #pragma unroll
     for (int r = 0; r < 4; r++) {
       const int64_t j = base + tok + 4 * w + r;
-      if (f.page >= 0 && j >= lo && j < hi) keep |= 255u << (8 * r);
+      if (f.vpage >= 0 && j >= lo && j < hi) keep |= 255u << (8 * r);
     }
-#pragma unroll
-    for (int r = 0; r < C::ROWS; r++) f.s[r][w] &= keep;
+    f.vs[w] &= keep;
   }
 }
 
-// Unit U (8 tokens of a channel pair) of a tile's values into LDS.
+// Unit U of a tile's decode into LDS: a code dword of the keys, then pieces of
+// the values.
 template <int U, int MODE, int D>
-__device__ __forceinline__ void store_value(const TileValues<MODE, D>& f, TileLds<D>& lds, int buf) {
-  using C = TileValues<MODE, D>;
-  constexpr int Y = C::TOK / 8, r = U / Y, y = U % Y;
+__device__ __forceinline__ void store_unit(const TileCodes<MODE, D>& f, TileLds<D>& lds, int buf) {
+  using C = TileCodes<MODE, D>;
+  using L = TileLds<D>;
   const int t = (int)threadIdx.x;
-  u32x4_t even, odd;
-  value_operands<MODE>(f.v[r][2 * y], f.v[r][2 * y + 1], f.s[r][2 * y], f.s[r][2 * y + 1], even, odd);
-  uint8_t* o = lds.v[buf] + ((t % C::TG) * Y + y) * TileLds<D>::VS +
-               (t / C::TG + r * (kThreads / C::TG)) * 16;
-  *(u32x4_t*)o = even;
-  *(u32x4_t*)(o + D / 2 * 16) = odd;
+  if constexpr (U < C::W) {
+    *(u32x4_t*)(lds.k[buf] + ((t & 7) * C::W + U) * L::KS + (t >> 3) * 16) =
+        key_operand<MODE, U * 8 / C::G>(f.k[U], f.ks);
+  } else {
+    constexpr int y = U - C::W, lo = D == 64 ? 0 : 2 * y, hi = D == 64 ? 0 : 2 * y + 1;
+    const int tok = (t % C::TG) * C::TOK + 8 * y;
+    u32x4_t even, odd;
+    value_operands<MODE>(f.v[lo], f.v[hi], f.vs[lo], f.vs[hi], even, odd);
+    uint8_t* o = lds.v[buf] + (tok / 8) * L::VS + (t / C::TG) * 16 + (tok % 8) * 2;
+    if constexpr (D == 64) {             // 4 tokens
+      *(u32x2_t*)o = u32x2_t{even[0], even[1]};
+      *(u32x2_t*)(o + D / 2 * 16) = u32x2_t{odd[0], odd[1]};
+    } else {
+      *(u32x4_t*)o = even;
+      *(u32x4_t*)(o + D / 2 * 16) = odd;
+    }
+  }
 }
 
 __device__ __forceinline__ float half_max(float v) {
@@ -162,7 +150,7 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 template <int MODE, int D, bool WIDE>
-__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) void kv_tiled_kernel(AttnArgs a) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f, kLag = MODE == 2 ? 8.0f : 3.0f;
   constexpr int QS = D / 16, NT = D / 32;
   using L = TileLds<D>;
@@ -184,9 +172,9 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
   auto lo_of = [&](int hi) { return a.window > 0 && hi > a.window ? hi - a.window : 0; };
   auto end_of = [&](uint32_t row) { return row < rt.rows ? row : rt.rows - 1; };
   const int tlo = lo_of(hi_of(rt.row0)), thi = hi_of(end_of(rt.row0 + kTileRows - 1));
-  const int64_t base0 = tlo & ~(kAttnKeys - 1);
+  const int64_t base0 = tlo & ~(kTileKeys - 1);
   const uint32_t blocks =
-      a.c.pages > 0 && thi > tlo ? ((uint32_t)(thi - base0) + kAttnKeys - 1) / kAttnKeys : 0;
+      a.c.pages > 0 && thi > tlo ? ((uint32_t)(thi - base0) + kTileKeys - 1) / kTileKeys : 0;
   const uint32_t per = (blocks + rt.parts - 1) / rt.parts;
   const uint32_t first = split * per;
   const uint32_t end = first + per < blocks ? first + per : blocks;
@@ -217,67 +205,48 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
   // row c of a key tile is the key that puts 8 consecutive ones into a lane's weights
   const int krow = (c & 16) | ((c & 4) << 1) | ((c & 8) >> 1) | (c & 3);
 
-  constexpr int kAhead = D == 256 ? 3 : 4;   // operands are read this many products early
-  using TK = TileKeys<MODE, D>;
-  using TV = TileValues<MODE, D>;
+  constexpr int kAhead = MODE == 2 ? 2 : 3;          // operands are read this many products early
   auto key_at = [&](int buf, int i) {
-    return *(const u32x4_t*)(lds.k[buf] + (2 * (i % QS) + hh) * L::KS + (32 * (i / QS) + krow) * 16);
+    return *(const u32x4_t*)(lds.k[buf] + (2 * i + hh) * L::KS + krow * 16);
   };
   auto value_at = [&](int buf, int i) {
     return *(const u32x4_t*)(lds.v[buf] + (2 * (i / NT) + hh) * L::VS + (32 * (i % NT) + c) * 16);
   };
   const bool alive = w0 < rt.rows;       // a wave without rows only decodes
-  TK kf;
-  TV vf;
-  constexpr int UNITS = TK::W + TV::UNITS;
-  auto store = [&](auto uu, int buf) {   // unit u of the decode
-    constexpr int u = decltype(uu)::value;
-    if constexpr (u < TK::W) store_key<u>(kf, lds, buf);
-    else store_value<u - TK::W>(vf, lds, buf);
-  };
+  using C = TileCodes<MODE, D>;
+  C f;
 
   // one tile: its scores while the next is decoded, its weights, its values
   auto tile = [&](int buf, int64_t base) {
-    f32x16_t s[2];
+    f32x16_t s;
     u32x4_t ring[kAhead];
     static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = key_at(buf, decltype(ii)::value); });
-    __builtin_amdgcn_sched_barrier(0);
-    static_for<2 * QS>([&](auto ii) {
-      constexpr int i = decltype(ii)::value, u0 = i * UNITS / (2 * QS), u1 = (i + 1) * UNITS / (2 * QS);
-      if constexpr (i % QS == 0) {
 #pragma unroll
-        for (int r = 0; r < 16; r++) s[i / QS][r] = 0.0f;
-      }
-      s[i / QS] = mfma32<MODE>(ring[i % kAhead], q[i % QS], s[i / QS]);
-      if constexpr (i + kAhead < 2 * QS) ring[i % kAhead] = key_at(buf, i + kAhead);
-      static_for<u1 - u0>([&](auto kk) {
-        store(std::integral_constant<int, u0 + decltype(kk)::value>{}, buf ^ 1);
-      });
+    for (int r = 0; r < 16; r++) s[r] = 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<QS>([&](auto ii) {
+      constexpr int i = decltype(ii)::value, u0 = i * C::UNITS / QS, u1 = (i + 1) * C::UNITS / QS;
+      s = mfma32<MODE>(ring[i % kAhead], q[i], s);
+      if constexpr (i + kAhead < QS) ring[i % kAhead] = key_at(buf, i + kAhead);
+      static_for<u1 - u0>([&](auto kk) { store_unit<u0 + decltype(kk)::value>(f, lds, buf ^ 1); });
       __builtin_amdgcn_sched_barrier(0);
     });
-    const int4 ok = *(const int4*)lds.ok[buf];
+    const int2 ok = *(const int2*)lds.ok[buf];
     static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = value_at(buf, decltype(ii)::value); });
     if (a.cap > 0.0f) {
 #pragma unroll
-      for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) s[kt][r] = capped(s[kt][r], sc.in);
+      for (int r = 0; r < 16; r++) s[r] = capped(s[r], sc.in);
     }
-    if (base < wlmax || base + 64 > whmin || !(ok.x & ok.y & ok.z & ok.w)) {
-      const int oks[4] = {ok.x, ok.y, ok.z, ok.w};
+    if (base < wlmax || base + kTileKeys > whmin || !(ok.x & ok.y)) {
 #pragma unroll
-      for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-          const int key = (int)base + 32 * kt + 16 * (r >> 3) + 8 * hh + (r & 7);
-          s[kt][r] = !oks[2 * kt + (r >> 3)] || key < lo || key >= hi ? -__builtin_inff() : s[kt][r];
-        }
+      for (int r = 0; r < 16; r++) {
+        const int key = (int)base + 16 * (r >> 3) + 8 * hh + (r & 7);
+        s[r] = !(r < 8 ? ok.x : ok.y) || key < lo || key >= hi ? -__builtin_inff() : s[r];
+      }
     }
-    float mx = s[0][0];
+    float mx = s[0];
 #pragma unroll
-    for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[kt][r]);
+    for (int r = 1; r < 16; r++) mx = fmaxf(mx, s[r]);
     mx = fmaxf(m, __builtin_fmaf(half_max(mx), sc.f, sc.off));
     if (__any(mx > m + kLag)) {
       const float fac = mx > m ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
@@ -291,12 +260,12 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
     const float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff - sc.off;
     // weights two at a time (pair j); a pair's arguments, exponentials and sum
     // are taken in three successive places
-    u32x4_t p[4];
+    u32x4_t p[2];
     float x0, x1, e0 = 0.0f, e1 = 0.0f;
     auto args = [&](auto jj) {
       constexpr int r = 2 * decltype(jj)::value;
-      x0 = __builtin_fmaf(s[r >> 4][r & 15], sc.f, -ref);
-      x1 = __builtin_fmaf(s[r >> 4][(r & 15) + 1], sc.f, -ref);
+      x0 = __builtin_fmaf(s[r], sc.f, -ref);
+      x1 = __builtin_fmaf(s[r + 1], sc.f, -ref);
     };
     auto pack = [&](auto jj) {
       constexpr int j = decltype(jj)::value;
@@ -309,24 +278,23 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
     };
     auto weight = [&](auto jj) {
       constexpr int j = decltype(jj)::value;
-      if constexpr (j % 8 > 0) pack(std::integral_constant<int, j - 1>{});
+      if constexpr (j % 4 > 0) pack(std::integral_constant<int, j - 1>{});
       e0 = __builtin_amdgcn_exp2f(x0);
       e1 = __builtin_amdgcn_exp2f(x1);
-      if constexpr (j % 8 < 7) args(std::integral_constant<int, j + 1>{});
+      if constexpr (j % 4 < 3) args(std::integral_constant<int, j + 1>{});
     };
     args(std::integral_constant<int, 0>{});
-    static_for<8>(weight);
-    pack(std::integral_constant<int, 7>{});
-    args(std::integral_constant<int, 8>{});
+    static_for<4>(weight);
+    pack(std::integral_constant<int, 3>{});
+    args(std::integral_constant<int, 4>{});
     __builtin_amdgcn_sched_barrier(0);
-    constexpr int N = 4 * NT;
-    static_for<N>([&](auto ii) {
-      constexpr int i = decltype(ii)::value, w0 = i * 16 / N, w1 = (i + 1) * 16 / N;
+    static_for<2 * NT>([&](auto ii) {
+      constexpr int i = decltype(ii)::value, j0 = i * 4 / NT, j1 = (i + 1) * 4 / NT;
       o[i % NT] = mfma32<MODE>(ring[i % kAhead], p[i / NT], o[i % NT]);
-      if constexpr (i + kAhead < N) ring[i % kAhead] = value_at(buf, i + kAhead);
-      if constexpr (i < N / 2) {
-        static_for<w1 - w0>([&](auto kk) { weight(std::integral_constant<int, 8 + w0 + decltype(kk)::value>{}); });
-        if constexpr (i == N / 2 - 1) pack(std::integral_constant<int, 15>{});
+      if constexpr (i + kAhead < 2 * NT) ring[i % kAhead] = value_at(buf, i + kAhead);
+      if constexpr (i < NT) {
+        static_for<j1 - j0>([&](auto kk) { weight(std::integral_constant<int, 4 + j0 + decltype(kk)::value>{}); });
+        if constexpr (i == NT - 1) pack(std::integral_constant<int, 7>{});
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -336,31 +304,33 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv_tiled_kernel(Att
   // keeps the loop free of cases; nothing uses them.
   if (first < end) {
     const uint32_t count = end - first;
-    auto base_of = [&](uint32_t i) { return base0 + (int64_t)(first + i) * kAttnKeys; };
+    auto base_of = [&](uint32_t i) { return base0 + (int64_t)(first + i) * kTileKeys; };
     auto key_page = [&](uint32_t i) {
-      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x >> 2));
+      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x >> 3));
     };
     auto value_page = [&](uint32_t i) {
-      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x % TV::TG * TV::TOK));
+      return page_id(a, rt.b, base_of(i) + (int)threadIdx.x % C::TG * C::TOK);
     };
     auto load = [&](uint32_t i, int kp, int vp) {
-      load_tile_keys<MODE, D, WIDE>(a, h, base_of(i), kp, kf);
-      load_tile_values<MODE, D, WIDE>(a, h, base_of(i), vp, vf);
+      load_tile<MODE, D, WIDE>(a, h, base_of(i), kp, vp, f);
     };
     auto ready = [&](uint32_t i) {       // what the decode of tile i needs once
-      drop_values(vf, base_of(i), tlo, thi);
-      if (lane == 0) lds.ok[i & 1][wave] = kf.page >= 0;
+      drop_values(f, base_of(i), tlo, thi);
+      if (lane == 0) lds.ok[i & 1][wave >> 1] = f.kpage >= 0;    // 8 keys a wave
     };
-    auto store_all = [&](int buf) { static_for<UNITS>([&](auto u) { store(u, buf); }); };
-    load(0, key_page(0), value_page(0));
-    int kp = key_page(1), vp = value_page(1);
+    auto store_all = [&](int buf) {
+      static_for<C::UNITS>([&](auto u) { store_unit<decltype(u)::value>(f, lds, buf); });
+    };
+    int kp = key_page(0), vp = WIDE ? kp : value_page(0);
+    load(0, kp, vp);
+    kp = key_page(1), vp = WIDE ? kp : value_page(1);
     ready(0);
     store_all(0);
     load(1, kp, vp);
     for (uint32_t i = 0; i < count; i++) {
       const int buf = (int)i & 1;
       kp = key_page(i + 2);
-      vp = value_page(i + 2);
+      vp = WIDE ? kp : value_page(i + 2);
       __syncthreads();                   // tile i is decoded, the other buffer free
       ready(i + 1);
       if (alive) tile(buf, base_of(i));

@@ -128,8 +128,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_kernel(RopeArgs a, 
   const int64_t tok = item / a.chunks;
   const int h0 = (int)(item - tok * a.chunks) * a.hpg;
   const int h1 = min(h0 + a.hpg, a.hq + a.hk);
-  Turn<INTER> turn;
-  turn.load(a, table_row(a, tok), sub);
+  const int64_t trow = table_row(a, tok);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   auto load = [&](int h) {
     const uint16_t* x = (h < a.hq ? a.q : a.k) + head_off(a, tok, h, a.qs, a.ks);
@@ -140,6 +139,8 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_kernel(RopeArgs a, 
   };
   const uint4 wq = weight(a.qw), wk = weight(a.kw);
   uint4 next = load(h0);
+  Turn<INTER> turn;                      // its rows wait for the position: last
+  turn.load(a, trow, sub);
   for (int h = h0; h < h1; h++) {
     const uint4 raw = next;
     if (h + 1 < h1) next = load(h + 1);
@@ -180,8 +181,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
     const int64_t tok = item / a.chunks;
     const int h0 = (int)(item - tok * a.chunks) * a.hpg;
     const int h1 = min(h0 + a.hpg, a.hq + a.hk);
-    Turn<INTER> turn;
-    turn.load(a, table_row(a, tok), sub);
+    const int64_t trow = table_row(a, tok);
     auto load_x = [&](int h) {
       const uint16_t* x = (h < a.hq ? a.q : a.k) + head_off(a, tok, h, a.qs, a.ks);
       return live ? *(const uint4*)(x + sub * 8) : zero;
@@ -191,6 +191,8 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
       return live ? *(const uint4*)(g + sub * 8) : zero;
     };
     uint4 nx = load_x(h0), ng = load_g(h0);
+    Turn<INTER> turn;
+    turn.load(a, trow, sub);
     for (int h = h0; h < h1; h++) {
       const uint4 rx = nx, rg = ng;
       if (h + 1 < h1) {
