@@ -107,11 +107,17 @@ hipError_t rope_variant(const fp4_qk_rope* a, F&& f) {
   }
 }
 
-// Workgroups of the backward pass: the rows of partial weight gradients.
+// Workgroups of the backward pass: the rows of partial weight gradients, which
+// a second launch joins; one writes the gradients itself.
+constexpr int kRopeAlone = 4;
 int64_t rope_bwd_groups(const fp4_qk_rope* a, const RopeArgs& r) {
   const int64_t per = kRopeThreads / lanes_per_head(a->head_dim);
   const int64_t g = cdiv(a->tokens * r.chunks, per);
-  return g < 1 ? 1 : (g < kRopeMaxGroups ? g : kRopeMaxGroups);
+  // a few rounds of one workgroup cost less than the second launch that joins
+  // several (40 heads of 128 of one token, forward and backward: 13.0 us, two
+  // launches 15.3; 4 tokens in 10 rounds: 21.1 and 15.3)
+  if (g <= kRopeAlone) return 1;
+  return g < kRopeMaxGroups ? g : kRopeMaxGroups;
 }
 
 // ------------------------------------------------------------------ attention
@@ -176,7 +182,11 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + wide : 1))
                                : (p.nt == 2 || d == 256 ? 2 : (d == 128 ? 3 : 4));
   p.want = cdiv(per_cu * (int64_t)num_cus(), c->heads);
-  const int64_t share = cdiv(4 * p.want, p.tiles), room = cdiv(blocks, 4);
+  // One part, without the launch that joins several, as long as a wave has two
+  // blocks at most: a context of 512 tokens 7.8 us (parts 9.4), of 768 9.4
+  // (9.4), of 1024 10.9 (9.7).
+  const int64_t share = cdiv(4 * p.want, p.tiles);
+  const int64_t room = p.nt && blocks <= 8 ? 1 : cdiv(blocks, 4);
   p.splits = p.tiles >= p.want ? 1 : (share < room ? share : room);
   p.splits = p.splits < 1 ? 1 : (p.splits > 64 ? 64 : p.splits);
   // every tile has one part and the rest come to a.want together
@@ -274,9 +284,10 @@ int qk_norm_rope_backward(const fp4_qk_rope* a, const uint16_t* dq_out, int64_t 
     e = rope_variant(a, [&](auto lph, auto inter) {
       return launch(qk_norm_rope_bwd_kernel<decltype(lph)::value, decltype(inter)::value>,
                     (unsigned)groups, kRopeThreads, st, r, dq_out, dq_out_stride, dk_out,
-                    dk_out_stride, dq, dq_stride, dk, dk_stride, want_w ? (float*)ws : nullptr);
+                    dk_out_stride, dq, dq_stride, dk, dk_stride,
+                    want_w && groups > 1 ? (float*)ws : nullptr, dq_weight, dk_weight);
     });
-  if (want_w)
+  if (want_w && groups != 1)
     e = first(e, launch(qk_norm_rope_dw_kernel, (unsigned)cdiv(2 * a->head_dim, kDwCols), kDwThreads,
                         st, (const float*)ws, (int)groups, a->head_dim, dq_weight, dk_weight));
   return launched(e);

@@ -161,11 +161,12 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_kernel(RopeArgs a, 
   }
 }
 
-// Partial weight gradients of workgroup b go to partial[b][0 = q, 1 = k][dim].
+// Partial weight gradients of workgroup b go to partial[b][0 = q, 1 = k][dim],
+// or without it (one workgroup) the gradients to dqw and dkw.
 template <int LPH, bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
     RopeArgs a, const uint16_t* dqo, int64_t dqos, const uint16_t* dko, int64_t dkos, uint16_t* dq,
-    int64_t dqs, uint16_t* dk, int64_t dks, float* partial) {
+    int64_t dqs, uint16_t* dk, int64_t dks, float* partial, float* dqw, float* dkw) {
   __shared__ float red[kRopeThreads / LPH][2][LPH * 8];
   const int sub = (int)threadIdx.x & (LPH - 1), grp = (int)threadIdx.x / LPH;
   const bool live = sub * 8 < a.dim;
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
       if (live) *(uint4*)(y + sub * 8) = pack8(g);
     }
   }
-  if (!partial) return;
+  if (!partial && !dqw && !dkw) return;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     red[grp][0][sub * 8 + i] = gq[i];
@@ -237,9 +238,15 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
   __syncthreads();
   for (int j = (int)threadIdx.x; j < 2 * a.dim; j += kRopeThreads) {
     const int which = j >= a.dim, c = which ? j - a.dim : j;
-    float t = 0.0f;
-    for (int g = 0; g < kRopeThreads / LPH; g++) t += red[g][which][c];
-    partial[(int64_t)blockIdx.x * 2 * a.dim + j] = t;
+    if (partial) {
+      float t = 0.0f;
+      for (int g = 0; g < kRopeThreads / LPH; g++) t += red[g][which][c];
+      partial[(int64_t)blockIdx.x * 2 * a.dim + j] = t;
+    } else if (float* out = which ? dkw : dqw) {
+      double t = 0.0;
+      for (int g = 0; g < kRopeThreads / LPH; g++) t += (double)red[g][which][c];
+      out[c] = (float)t;
+    }
   }
 }
 
