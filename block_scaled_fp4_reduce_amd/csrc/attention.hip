@@ -219,10 +219,11 @@ hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st
     else if constexpr (D < 256) e = go(std::integral_constant<int, 2>{});
   }
   if (p.splits > 1) {
-    // as many lanes on a row's parts as leave a lane 4 of them
+    // as many lanes on a row's parts as leave a lane 4 of the even share
     const int lanes = D / 4, most = kThreads / lanes;
+    const int64_t share = cdiv(p.want, p.tiles), parts = share < p.splits ? share : p.splits;
     int groups = 1;
-    while (groups < most && groups * 4 < p.splits) groups *= 2;
+    while (groups < most && groups * 4 < parts) groups *= 2;
     e = first(e, launch(kv_attention_join_kernel<MODE, D>,
                         (unsigned)cdiv(a.tokens * a.hq, kThreads / (lanes * groups)), kThreads, st,
                         a, groups, a.tokens * a.hq <= 4096));

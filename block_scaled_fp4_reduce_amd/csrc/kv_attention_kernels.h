@@ -803,7 +803,8 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
       float4 y[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        const int64_t s = min(s0 + e * groups, most - 1);
+        const int64_t s = s0 + e * groups;
+        if (s >= most) continue;
         ml[e] = *(const float2*)(a.pm + (s * rows + row) * 2);
         y[e] = *(const float4*)(a.po + (s * rows + row) * D + lane * 4);
       }
