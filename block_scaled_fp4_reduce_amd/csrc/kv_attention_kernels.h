@@ -25,6 +25,18 @@
 // (fp16) or 2^-7 (bf16) of each: the sum over the row uses the unrounded
 // ones, and the accumulators are fp32.  fp16 weights carry a factor 2^12,
 // so that only those under 2^-26 of the largest lose bits.
+//
+// The kernel here is for few rows (up to 32 a sequence and kv head; the tiled
+// one takes more): a wave decodes 64 keys and values straight into its operand
+// registers, so every cached byte is read once and nothing goes through LDS
+// but the queries.  A wave loads its next keys as soon as the first product
+// has read the registers and its next values after the second; at D = 128
+// three waves a SIMD (160 registers) hide the rest.  Memory bounds it: 64
+// sequences of 2048 to 8192 tokens (8 kv heads, NVFP4 4/6, 379 MB) in 94 us
+// of calls, 4.0 TB/s, where a large copy moves 4.85; 2 sequences up to 131072
+// (MXFP4, 219 MB) in 53 us.  Vector instructions issue in 45% of the cycles.
+// Short contexts are all latency: 2048 tokens of one sequence 7.2 us and 3.2
+// to 3.8 for the join, in 10.3 us a call.
 #pragma once
 
 #include "kv_common.h"

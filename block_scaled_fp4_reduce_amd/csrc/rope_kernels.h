@@ -14,6 +14,11 @@
 // half-split rotation sits rot/16 lanes away.  A group takes several heads
 // of one token, so the token's cosines and sines are read once for them.
 // Everything is fp32 until the one rounding to bf16 at the store.
+//
+// Memory bounds it: 8192 tokens of 40 heads of 128 (84 MB a tensor) forward
+// in 33.8 us (5.0 TB/s), backward in 52.7 (4.8 TB/s) and 5.0 for the join of
+// the weight gradients.  With one head per lane group the cosines are read
+// for every head and the pair takes 170 us instead of 93.
 #pragma once
 
 #include "kv_common.h"

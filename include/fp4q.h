@@ -340,7 +340,9 @@ size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_
  * nothing (kv_len 0, or fewer cached tokens than new ones) gets out = 0 and
  * lse = -inf.  Cached bytes past a sequence's length are never looked at,
  * whatever they hold; a page id outside the cache contributes nothing; a
- * length past the table is cut to it. */
+ * length past the table is cut to it.  out may not overlap q; tokens times
+ * q_heads, and sequences times q_heads, stay below 2^31.  Equal calls give
+ * equal bits. */
 int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_queries* x, uint16_t* out,
                      int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
 
