@@ -312,27 +312,44 @@ struct KvPages {
   int k, v;
 };
 
-__device__ __forceinline__ int page_id(const AttnArgs& a, uint32_t b, int64_t key) {
-  const int64_t i = key >> a.c.page_shift;
-  if (i >= a.width) return -1;
-  const int p = a.pt[b * a.width + i];
-  return p >= 0 && p < a.c.pages ? p : -1;
-}
+// A sequence's row of the page table.  Keys, table width and pages stay below
+// 2^31 (the host checks them), so a key's place is 32-bit arithmetic; keys of
+// blocks past the end pass 2^31 by a few blocks at most and fit as unsigned.
+struct PageRow {
+  const ConstInt* row;
+  uint32_t width, pages;
+  int shift;
+  __device__ __forceinline__ PageRow(const AttnArgs& a, uint32_t b)
+      : row(a.pt + b * a.width), width((uint32_t)a.width), pages((uint32_t)a.c.pages),
+        shift(a.c.page_shift) {}
+  __device__ __forceinline__ int at(uint32_t key) const {
+    const uint32_t i = key >> shift;
+    if (i >= width) return -1;
+    const uint32_t p = (uint32_t)row[i];
+    return p < pages ? (int)p : -1;
+  }
+};
 
 // With pages of 64 tokens and more a block lies in one page, whose address is
 // the same for the whole wave (scalar arithmetic); with smaller ones each
 // lane follows its own.
 template <bool WIDE>
-__device__ __forceinline__ KvPages load_pages(const AttnArgs& a, uint32_t b, int64_t base) {
+__device__ __forceinline__ KvPages load_pages(const PageRow& r, uint32_t base) {
   const int lane = (int)threadIdx.x & 63;
   KvPages p;
   if constexpr (WIDE) {
-    p.k = p.v = page_id(a, b, base);
+    p.k = p.v = r.at(base);
   } else {
-    p.k = page_id(a, b, base + 16 * ((lane & 15) >> 2));
-    p.v = page_id(a, b, base + 16 * (lane >> 4));
+    p.k = r.at(base + 16 * ((lane & 15) >> 2));
+    p.v = r.at(base + 16 * (lane >> 4));
   }
   return p;
+}
+
+// Tokens before page `page` of head h, counted over the whole cache.
+__device__ __forceinline__ int64_t head_page(const AttnArgs& a, int h, int page) {
+  return (int64_t)((uint64_t)(uint32_t)(page < 0 ? 0 : page) * (uint32_t)a.c.heads + (uint32_t)h)
+         << a.c.page_shift;
 }
 
 // N bytes at `base` + `lane` + `step`, the first (and the step) the same for
@@ -363,14 +380,13 @@ struct KvLoad {
 };
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_keys(const AttnArgs& a, int h, int64_t base, KvPages pg,
+__device__ __forceinline__ void load_keys(const AttnArgs& a, int h, uint32_t base, KvPages pg,
                                           KeyFragment<MODE, D>& f) {
   constexpr int G = KeyFragment<MODE, D>::G, KD = D / 32;
   const int lane = (int)threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int P = 1 << a.c.page_shift, seg = 16 * (c >> 2);
-  const int64_t pk = (int64_t)(pg.k < 0 ? 0 : pg.k) * a.c.heads + h;
+  const uint32_t P = 1u << a.c.page_shift, seg = 16 * (c >> 2);
   // token of the page (the same for the wave when WIDE), and the lane's offset from it
-  const int64_t at = pk * P + (int)((WIDE ? base : base + seg) & (P - 1));
+  const int64_t at = head_page(a, h, pg.k) + ((WIDE ? base : base + seg) & (P - 1));
   const uint32_t row = (WIDE ? seg : 0) + (c & 3);
   const uint8_t* kc = a.c.kc + at * (D / 2);
   const uint8_t* ks = a.c.ks + at * (D / G);
@@ -390,16 +406,15 @@ __device__ __forceinline__ void load_keys(const AttnArgs& a, int h, int64_t base
 }
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_values(const AttnArgs& a, int h, int64_t base, KvPages pg,
+__device__ __forceinline__ void load_values(const AttnArgs& a, int h, uint32_t base, KvPages pg,
                                             ValueFragment<MODE, D>& f) {
   constexpr int G = KeyFragment<MODE, D>::G, KD = D / 32;
   const int lane = (int)threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int P = 1 << a.c.page_shift;
-  const int64_t pv = (int64_t)(pg.v < 0 ? 0 : pg.v) * a.c.heads + h;
-  const int at = (int)((WIDE ? base : base + 16 * g) & (P - 1));
-  const uint32_t tok = WIDE ? 16 * g : 0;
-  const uint8_t* vc = a.c.vc + pv * (D / 2) * P + at;
-  const uint8_t* vs = a.c.vs + pv * (D / G) * P + at;
+  const uint32_t P = 1u << a.c.page_shift;
+  const int64_t pv = head_page(a, h, pg.v);
+  const uint32_t at = (WIDE ? base : base + 16 * g) & (P - 1), tok = WIDE ? 16 * g : 0;
+  const uint8_t* vc = a.c.vc + pv * (D / 2) + at;
+  const uint8_t* vs = a.c.vs + pv * (D / G) + at;
   const uint32_t vo = ((uint32_t)c << a.c.page_shift) + tok;
   const uint32_t so = ((uint32_t)(MODE == 2 ? 0 : c >> 3) << a.c.page_shift) + tok;
 #pragma unroll
@@ -559,8 +574,8 @@ void kv_attention_kernel(AttnArgs a) {
   auto lo_of = [&](int hi) { return a.window > 0 && hi > a.window ? hi - a.window : 0; };
   const int hmin = hi_of(rt.row0), hmax = hi_of(last);
   const int lmin = lo_of(hmin), lmax = lo_of(hmax);
-  const int64_t base0 = lmin & ~(kAttnKeys - 1);
-  const uint32_t blocks = a.c.pages > 0 && hmax > lmin ? ((uint32_t)(hmax - base0) + kAttnKeys - 1) / kAttnKeys : 0;
+  const uint32_t base0 = (uint32_t)lmin & ~(uint32_t)(kAttnKeys - 1);
+  const uint32_t blocks = a.c.pages > 0 && hmax > lmin ? ((uint32_t)hmax - base0 + kAttnKeys - 1) / kAttnKeys : 0;
   const uint32_t per = (blocks + rt.parts - 1) / rt.parts;
   const uint32_t end = (split + 1) * per < blocks ? (split + 1) * per : blocks;
   if (a.splits > 1) {
@@ -595,11 +610,12 @@ void kv_attention_kernel(AttnArgs a) {
 
   KeyFragment<MODE, D> kf;
   ValueFragment<MODE, D> vf;
-  auto base_of = [&](uint32_t i) { return base0 + (int64_t)i * kAttnKeys; };
+  const PageRow pages(a, rt.b);
+  auto base_of = [&](uint32_t i) { return base0 + i * kAttnKeys; };
   // one block: its keys and values are in kf and vf; the next block's loads go out
   // as soon as the registers are free, keys after the first product, values
   // after the second
-  auto step = [&](int64_t base, KvPages pg, bool more, int64_t next, KvPages npg) {
+  auto step = [&](uint32_t base, KvPages pg, bool more, uint32_t next, KvPages npg) {
     f32x4_t s[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; i++)
@@ -631,7 +647,7 @@ void kv_attention_kernel(AttnArgs a) {
           for (int r = 0; r < 4; r++) s[i][t][r] = capped(s[i][t][r], sc[i].in);
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // bytes of the tokens that count
-    if (base < lmax || base + kAttnKeys > hmin || !__all(pg.v >= 0)) {
+    if (base < (uint32_t)lmax || base + kAttnKeys > (uint32_t)hmin || !__all(pg.v >= 0)) {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
         keep[t] = 0;
@@ -702,13 +718,13 @@ void kv_attention_kernel(AttnArgs a) {
 
   __syncthreads();                       // the queries are in LDS
   if (blk < end) {
-    KvPages pg = load_pages<WIDE>(a, rt.b, base_of(blk));
-    KvPages npg = load_pages<WIDE>(a, rt.b, base_of(blk + WAVES));
+    KvPages pg = load_pages<WIDE>(pages, base_of(blk));
+    KvPages npg = load_pages<WIDE>(pages, base_of(blk + WAVES));
     load_keys<MODE, D, WIDE>(a, h, base_of(blk), pg, kf);
     __builtin_amdgcn_sched_barrier(0);   // keys first, as in the loop: its waits count on it
     load_values<MODE, D, WIDE>(a, h, base_of(blk), pg, vf);
     for (; blk < end; blk += WAVES) {
-      const KvPages after = load_pages<WIDE>(a, rt.b, base_of(blk + 2 * WAVES));
+      const KvPages after = load_pages<WIDE>(pages, base_of(blk + 2 * WAVES));
       step(base_of(blk), pg, blk + WAVES < end, base_of(blk + WAVES), npg);
       pg = npg;
       npg = after;

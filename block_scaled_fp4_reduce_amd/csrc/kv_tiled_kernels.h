@@ -61,24 +61,25 @@ struct TileCodes {
 };
 
 template <int MODE, int D, bool WIDE>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int h, int64_t base, int kpage,
+__device__ __forceinline__ void load_tile(const AttnArgs& a, int h, uint32_t base, int kpage,
                                           int vpage, TileCodes<MODE, D>& f) {
   using C = TileCodes<MODE, D>;
   constexpr int G = C::G, SB = D / 8 >= G ? D / 8 / G : 1;
-  const int t = (int)threadIdx.x, shift = a.c.page_shift, P = 1 << shift, part = t & 7;
+  const int t = (int)threadIdx.x, shift = a.c.page_shift, part = t & 7;
+  const uint32_t P = 1u << shift;
   f.kpage = kpage;
   f.vpage = vpage;
   // page and token of it (the same for the wave when WIDE), and the lane's offset
-  const int64_t pk = (int64_t)(kpage < 0 ? 0 : kpage) * a.c.heads + h;
-  const int64_t at = (pk << shift) + (int)((WIDE ? base : base + (t >> 3)) & (P - 1));
+  const int64_t pk = head_page(a, h, kpage);
+  const int64_t at = pk + ((WIDE ? base : base + (t >> 3)) & (P - 1));
   const uint32_t row = WIDE ? t >> 3 : 0;
   const auto k = KvLoad<C::B, WIDE>::at(a.c.kc + at * (D / 2), row * (D / 2) + part * C::B, 0);
   f.ks = KvLoad<SB, WIDE>::at(a.c.ks + at * (D / G), row * (D / G) + part * (D / 8) / G, 0)[0];
-  const int64_t pv = WIDE ? pk : (int64_t)(vpage < 0 ? 0 : vpage) * a.c.heads + h;
-  const int tok = (t % C::TG) * C::TOK, av = (int)((WIDE ? base : base + tok) & (P - 1));
+  const int64_t pv = WIDE ? pk : head_page(a, h, vpage);
+  const uint32_t tok = (t % C::TG) * C::TOK, av = (WIDE ? base : base + tok) & (P - 1);
   const uint32_t i = t / C::TG, off = WIDE ? tok : 0;
-  const auto v = KvLoad<C::B, WIDE>::at(a.c.vc + ((pv * (D / 2)) << shift) + av, (i << shift) + off, 0);
-  const auto s = KvLoad<C::B, WIDE>::at(a.c.vs + ((pv * (D / G)) << shift) + av,
+  const auto v = KvLoad<C::B, WIDE>::at(a.c.vc + pv * (D / 2) + av, (i << shift) + off, 0);
+  const auto s = KvLoad<C::B, WIDE>::at(a.c.vs + pv * (D / G) + av,
                                         ((2 * i / G) << shift) + off, 0);
 #pragma unroll
   for (int e = 0; e < C::W; e++) {
@@ -99,7 +100,7 @@ struct TileLds {
 // Values of tokens outside [lo, hi) or without a page count as zeros: their
 // scales become zero.
 template <int MODE, int D>
-__device__ __forceinline__ void drop_values(TileCodes<MODE, D>& f, int64_t base, int lo, int hi) {
+__device__ __forceinline__ void drop_values(TileCodes<MODE, D>& f, uint32_t base, uint32_t lo, uint32_t hi) {
   using C = TileCodes<MODE, D>;
   if (base >= lo && base + kTileKeys <= hi && __all(f.vpage >= 0)) return;
   const int tok = ((int)threadIdx.x % C::TG) * C::TOK;
@@ -108,7 +109,7 @@ __device__ __forceinline__ void drop_values(TileCodes<MODE, D>& f, int64_t base,
     uint32_t keep = 0;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-      const int64_t j = base + tok + 4 * w + r;
+      const uint32_t j = base + tok + 4 * w + r;
       if (f.vpage >= 0 && j >= lo && j < hi) keep |= 255u << (8 * r);
     }
     f.vs[w] &= keep;
@@ -173,9 +174,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
   auto lo_of = [&](int hi) { return a.window > 0 && hi > a.window ? hi - a.window : 0; };
   auto end_of = [&](uint32_t row) { return row < rt.rows ? row : rt.rows - 1; };
   const int tlo = lo_of(hi_of(rt.row0)), thi = hi_of(end_of(rt.row0 + kTileRows - 1));
-  const int64_t base0 = tlo & ~(kTileKeys - 1);
+  const uint32_t base0 = (uint32_t)tlo & ~(uint32_t)(kTileKeys - 1);
   const uint32_t blocks =
-      a.c.pages > 0 && thi > tlo ? ((uint32_t)(thi - base0) + kTileKeys - 1) / kTileKeys : 0;
+      a.c.pages > 0 && thi > tlo ? ((uint32_t)thi - base0 + kTileKeys - 1) / kTileKeys : 0;
   const uint32_t per = (blocks + rt.parts - 1) / rt.parts;
   const uint32_t first = split * per;
   const uint32_t end = first + per < blocks ? first + per : blocks;
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
   // row c of a key tile is the key that puts 8 consecutive ones into a lane's weights
   const int krow = (c & 16) | ((c & 4) << 1) | ((c & 8) >> 1) | (c & 3);
 
-  constexpr int kAhead = MODE == 2 ? 2 : 3;          // operands are read this many products early
+  constexpr int kAhead = 2;              // operands are read this many products early
   auto key_at = [&](int buf, int i) {
     return *(const u32x4_t*)(lds.k[buf] + (2 * i + hh) * L::KS + krow * 16);
   };
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
   C f;
 
   // one tile: its scores while the next is decoded, its weights, its values
-  auto tile = [&](int buf, int64_t base) {
+  auto tile = [&](int buf, uint32_t base) {
     f32x16_t s;
     u32x4_t ring[kAhead];
     static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = key_at(buf, decltype(ii)::value); });
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
 #pragma unroll
       for (int r = 0; r < 16; r++) s[r] = capped(s[r], sc.in);
     }
-    if (base < wlmax || base + kTileKeys > whmin || !(ok.x & ok.y)) {
+    if (base < (uint32_t)wlmax || base + kTileKeys > (uint32_t)whmin || !(ok.x & ok.y)) {
 #pragma unroll
       for (int r = 0; r < 16; r++) {
         const int key = (int)base + 16 * (r >> 3) + 8 * hh + (r & 7);
@@ -305,12 +306,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
   // keeps the loop free of cases; nothing uses them.
   if (first < end) {
     const uint32_t count = end - first;
-    auto base_of = [&](uint32_t i) { return base0 + (int64_t)(first + i) * kTileKeys; };
+    const PageRow pages(a, rt.b);
+    auto base_of = [&](uint32_t i) { return base0 + (first + i) * kTileKeys; };
     auto key_page = [&](uint32_t i) {
-      return page_id(a, rt.b, base_of(i) + (WIDE ? 0 : (int)threadIdx.x >> 3));
+      return pages.at(base_of(i) + (WIDE ? 0 : threadIdx.x >> 3));
     };
     auto value_page = [&](uint32_t i) {
-      return page_id(a, rt.b, base_of(i) + (int)threadIdx.x % C::TG * C::TOK);
+      return pages.at(base_of(i) + threadIdx.x % C::TG * C::TOK);
     };
     auto load = [&](uint32_t i, int kp, int vp) {
       load_tile<MODE, D, WIDE>(a, h, base_of(i), kp, vp, f);
