@@ -507,16 +507,24 @@ int check_kv_tokens(const fp4_kv_cache* c, const void* k, int64_t k_stride, cons
 
 // f(mode, head_dim, tokens per workgroup) as compile-time constants, with the
 // grid of that tile.  64 tokens fill the 64-byte lines of a page's rows of
-// values; with too few tiles of 64 for the CUs, tiles of 16 spread the call
-// over more of them.
+// values and cost the least per token; fewer tiles of them than 16 a CU leave
+// its loads, arithmetic and stores waiting for each other, and fewer tiles of
+// 32 than 2 a CU leave CUs idle.  Write and read of heads of 128, NVFP4 4/6,
+// tiles of 64 / 32 / 16: 8192 tokens x 8 heads 15.0 + 9.9 / 13.6 + 9.1 / 13.1 +
+// 10.7 us, 1024 tokens 5.5 + 7.5 / 4.1 + 5.6 / 3.9 + 5.7; read of 65536 tokens
+// 72.6 / 73.4 / 86.8.
 template <typename F>
 int kv_variant(const fp4_kv_cache* c, int64_t tokens, F&& f) {
-  const int64_t tt = cdiv(tokens, 64) * c->heads >= 2 * num_cus() ? 64 : 16;
+  const int64_t tt = cdiv(tokens, 64) * c->heads >= 16 * num_cus() ? 64
+                     : cdiv(tokens, 32) * c->heads >= 2 * num_cus() ? 32 : 16;
   const int64_t grid = cdiv(tokens, tt) * c->heads;
   if (grid > (((int64_t)1 << 32) - 1) / kThreads) return FP4_E_SHAPE;
   auto tile = [&](auto mode, auto dim) {
-    return tt == 64 ? f(mode, dim, std::integral_constant<int, 64>{}, (unsigned)grid)
-                    : f(mode, dim, std::integral_constant<int, 16>{}, (unsigned)grid);
+    switch (tt) {
+      case 64: return f(mode, dim, std::integral_constant<int, 64>{}, (unsigned)grid);
+      case 32: return f(mode, dim, std::integral_constant<int, 32>{}, (unsigned)grid);
+      default: return f(mode, dim, std::integral_constant<int, 16>{}, (unsigned)grid);
+    }
   };
   auto head = [&](auto mode) {
     switch (c->head_dim) {
