@@ -138,3 +138,18 @@ def test_lse_is_optional_and_workspace_is_checked(new):
     again = fp4.fp4_kv_attention(*args, max_q=max(news), stream=side)
     side.synchronize()
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("page", [32, 64, 128])
+def test_bad_pages_of_whole_blocks(mode, new, page):
+    """Pages outside the cache where a block lies in one page: first, middle and
+    last ones contribute nothing, their neighbours everything."""
+    rng = np.random.default_rng(page + new)
+    lens, news = [9 * page, 9 * page - 5], [new, new]
+    ref, ka, pt, cu, qb = build(rng, mode, lens, news, 1, 4, 64, page)
+    pt[0, [0, 4, 8]] = [-1, ref["k_codes"].shape[0], 2 ** 31 - 1]
+    pt[1, [3, 5]] = -2 ** 31
+    got = run(mode, ref, ka, pt, lens, cu, qb, max_q=new)
+    check(mode, got, ref, ka, pt, lens, cu, qb)
