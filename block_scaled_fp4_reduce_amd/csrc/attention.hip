@@ -170,7 +170,8 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   p.tiles = x->cu_q ? x->tokens * group / m + x->seqs : x->seqs * cdiv(group, m);
   // keys in reach of a tile, at most
   int64_t keys = x->table_width * c->page_size;
-  if (x->window > 0 && keys > x->window + most) keys = x->window + most;
+  const int64_t span = most < m / group + 2 ? most : m / group + 2;    // new tokens of a tile
+  if (x->window > 0 && keys > x->window + span) keys = x->window + span;
   const int64_t blocks = cdiv(keys, kAttnKeys);
   // Workgroups wanted per kv head.  How they are shared out among the
   // sequences depends on lengths that only the device knows (item_of); a

@@ -163,7 +163,7 @@ __device__ __forceinline__ uint32_t tile_of(const AttnArgs& a, uint32_t t, Work&
   return t - (cu_at(a, w.b) * group / M + w.b);      // wraps to no tile before the first
 }
 
-// Blocks of 64 keys that `n` new tokens at the end of `len` can reach.
+// Blocks of 64 keys that a tile of `n` new tokens among `len` can reach.
 __device__ __forceinline__ uint32_t blocks_in_reach(const AttnArgs& a, int64_t len, int64_t n) {
   const int64_t most = a.width << a.c.page_shift;
   int64_t reach = len > most ? most : len;
@@ -215,7 +215,7 @@ __device__ __forceinline__ uint32_t item_of(const AttnArgs& a, uint32_t t, Work&
       n = in && c1 > c0 ? c1 - c0 : 0;
     }
     tiles = (n * (uint32_t)a.group + M - 1) / M;
-    blocks = blocks_in_reach(a, len, n);
+    blocks = blocks_in_reach(a, len, min(n, M / (uint32_t)a.group + 2));
   };
   float total = 0.0f;                    // tiles x blocks
   for (uint32_t first = 0; first < seqs; first += 64) {
