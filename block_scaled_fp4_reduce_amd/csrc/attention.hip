@@ -177,7 +177,7 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   // sequences depends on lengths that only the device knows (item_of); a
   // tile gets at most four times an even share.  As many as run at once (by
   // their registers), so that all of them end together: chunks of 512 tokens
-  // over 6144 cached, 3 to a CU: 171 us, 2: 209, 4: 203, 6: 200.
+  // over 6144 cached, 3 to a CU: 139 us, 2: 161, 4: 162, 6: 166.
   const bool wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   const int d = c->head_dim;
   const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + wide : 1))

@@ -31,12 +31,12 @@
 // registers, so every cached byte is read once and nothing goes through LDS
 // but the queries.  A wave loads its next keys as soon as the first product
 // has read the registers and its next values after the second; at D = 128
-// three waves a SIMD (160 registers) hide the rest.  Memory bounds it: 64
-// sequences of 2048 to 8192 tokens (8 kv heads, NVFP4 4/6, 379 MB) in 94 us
-// of calls, 4.0 TB/s, where a large copy moves 4.85; 2 sequences up to 131072
-// (MXFP4, 219 MB) in 53 us.  Vector instructions issue in 45% of the cycles.
-// Short contexts are all latency: 2048 tokens of one sequence 7.2 us and 3.2
-// to 3.8 for the join, in 10.3 us a call.
+// three waves a SIMD (150 registers) hide the rest.  Memory bounds it: 64
+// sequences of 2048 to 8192 tokens (8 kv heads, NVFP4 4/6, 379 MB) in 93 us
+// of calls, 4.1 TB/s, where a large copy moves 4.85; 2 sequences up to 131072
+// (MXFP4, 219 MB) in 53 us.  Vector instructions issue in 46% of the cycles.
+// Short contexts are all latency: 2048 tokens of one sequence 7.2 us and 3.1
+// to 3.9 for the join, in 10.1 us a call.
 #pragma once
 
 #include "kv_common.h"

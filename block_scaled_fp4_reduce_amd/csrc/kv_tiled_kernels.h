@@ -13,13 +13,14 @@
 // products of the first half's values (double buffers, one barrier per tile).
 // Tiles of 32 keys keep the registers of a wave at 168, so that three run on
 // a SIMD.  Vector instructions bound it: counted at D = 128, MXFP4, capped,
-// they issue in 71% of the cycles and the matrix unit runs in 33%.
+// they issue in 74% of the cycles and the matrix unit runs in 36%.
 //
 // Measured, D = 128, 32 query and 8 kv heads: a prompt of 8192 tokens, window
-// 4096, capped, MXFP4: 516 us (799 TFLOP/s of the products); 4 sequences with
-// up to 512 new tokens over 6144, NVFP4 4/6: 149 us with the join (671
-// TFLOP/s).  Tiles of 64 keys and two waves a SIMD: 6% slower on the chunks,
-// the same on the prompt.
+// 4096, capped, MXFP4: 491 us (840 TFLOP/s of the products); 4 sequences with
+// up to 512 new tokens over 6144, NVFP4 4/6: 138 us with the join (722
+// TFLOP/s).  When they were measured side by side (522 and 158 us then), tiles
+// of 64 keys and two waves a SIMD took the same on the prompt and 169 us on the
+// chunks.
 //
 // LDS layout: 16-byte chunks, column after column, so that a wave's operand
 // reads are contiguous.  Keys: chunk (channels 8 x .. 8 x + 7, key).  Values:
