@@ -157,13 +157,15 @@ int check_attention(const fp4_kv_cache* c, const fp4_kv_queries* x, const uint16
 // context.
 struct AttnPlan {
   int nt;
+  bool wide;                             // a block of keys lies in one page
   int64_t tiles, splits, want, places;
 };
 
 AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   AttnPlan p;
   const int64_t group = x->q_heads / c->heads;
-  const int64_t most = !x->cu_q ? 1 : (x->max_q > 0 ? x->max_q : cdiv(x->tokens, x->seqs));
+  const int64_t known = x->max_q < x->tokens ? x->max_q : x->tokens;
+  const int64_t most = !x->cu_q ? 1 : (known > 0 ? known : cdiv(x->tokens, x->seqs));
   const int64_t rows = most * group;
   p.nt = rows <= 16 ? 1 : (rows <= 32 && c->head_dim < 256 ? 2 : 0);
   const int64_t m = p.nt ? 16 * p.nt : kTileRows;
@@ -178,9 +180,9 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   // tile gets at most four times an even share.  As many as run at once (by
   // their registers), so that all of them end together: chunks of 512 tokens
   // over 6144 cached, 3 to a CU: 139 us, 2: 161, 4: 162, 6: 166.
-  const bool wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
+  p.wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   const int d = c->head_dim;
-  const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + wide : 1))
+  const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + p.wide : 1))
                                : (p.nt == 2 || d == 256 ? 2 : (d == 128 ? 3 : 4));
   p.want = cdiv(per_cu * (int64_t)num_cus(), c->heads);
   // One part, without the launch that joins several, as long as a wave has two
@@ -204,17 +206,15 @@ size_t attention_ws(const fp4_kv_cache* c, const fp4_kv_queries* x, const AttnPl
 template <int MODE, int D>
 hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)(p.places * a.c.heads);
-  // a block of keys lies in one page
-  const bool wide = (1 << a.c.page_shift) >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
-    e = wide ? launch(kv_tiled_kernel<MODE, D, true>, grid, kThreads, st, a)
-             : launch(kv_tiled_kernel<MODE, D, false>, grid, kThreads, st, a);
+    e = p.wide ? launch(kv_tiled_kernel<MODE, D, true>, grid, kThreads, st, a)
+               : launch(kv_tiled_kernel<MODE, D, false>, grid, kThreads, st, a);
   } else {
     auto go = [&](auto nt) {
       constexpr int N = decltype(nt)::value;
-      return wide ? launch(kv_attention_kernel<MODE, D, N, 4, true>, grid, 256, st, a)
-                  : launch(kv_attention_kernel<MODE, D, N, 4, false>, grid, 256, st, a);
+      return p.wide ? launch(kv_attention_kernel<MODE, D, N, 4, true>, grid, 256, st, a)
+                    : launch(kv_attention_kernel<MODE, D, N, 4, false>, grid, 256, st, a);
     };
     if (p.nt == 1) e = go(std::integral_constant<int, 1>{});
     else if constexpr (D < 256) e = go(std::integral_constant<int, 2>{});

@@ -71,3 +71,10 @@ def test_rows_are_counted_in_32_bits():
     x = fp4._CQueries(p, 65536 * 64, 1 << 20, 1 << 20, None, 0, p, p, 5, 65536, 0, 0.1, 0.0)
     assert fp4.lib().fp4_kv_attention(c, x, p, 65536 * 64, None, p, 1 << 40, None) == -2
     assert fp4.lib().fp4_kv_attention_workspace_bytes(c, x) == 0
+
+
+def test_any_hint_of_new_tokens_plans_the_call():
+    c, p = Handle()._c, 0x10000
+    for hint in (0, 1, 6, 7, 1 << 62):
+        x = fp4._CQueries(p, 256, 6, 3, p, hint, p, p, 40, 4, 0, 0.1, 0.0)
+        assert 0 <= fp4.lib().fp4_kv_attention_workspace_bytes(c, x) < 1 << 24
