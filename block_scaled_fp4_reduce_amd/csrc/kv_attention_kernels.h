@@ -542,6 +542,20 @@ __device__ __forceinline__ float capped(float x, float in) {
   return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x * in));
 }
 
+// The weight of a score is exp2(f x - (m - off - kOff)) in one fma, whose exact
+// product keeps what m lost in its rounding: a sixteenth at kFarMax, but from
+// about 2^25 on more than the weights' exponents hold.  Past kFarMax a lane's
+// scores are rounded as m was and replaced by their distances to it, over f, so
+// that the same fma with the reference -kOff gives the weight.
+constexpr float kFarMax = 0x1p20f;
+template <typename V>
+__device__ __forceinline__ void far_scores(const ScoreScale& sc, float m, V& s) {
+  const float rf = __builtin_amdgcn_rcpf(sc.f);
+#pragma unroll
+  for (int r = 0; r < (int)(sizeof(V) / sizeof(float)); r++)
+    s[r] = (__builtin_fmaf(s[r], sc.f, sc.off) - m) * rf;
+}
+
 // NT columns of 16 query rows, WAVES waves that take the blocks of 64 keys of
 // the workgroup's part of the context in turn and join their sums at the end.
 template <int MODE, int D, int NT, int WAVES, bool WIDE>
@@ -682,7 +696,12 @@ void kv_attention_kernel(AttnArgs a) {
           }
         m[i] = mx;
       }
-      const float ref = (m[i] == -__builtin_inff() ? 0.0f : m[i]) - kOff - sc[i].off;
+      float ref = (m[i] == -__builtin_inff() ? 0.0f : m[i]) - kOff - sc[i].off;
+      if (fabsf(ref) > kFarMax) {
+#pragma unroll
+        for (int t = 0; t < 4; t++) far_scores(sc[i], m[i], s[i][t]);
+        ref = -kOff;
+      }
 #pragma unroll
       for (int t = 0; t < 4; t++) {
         float e[4];

@@ -269,7 +269,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
         for (int r = 0; r < 16; r++) o[T][r] *= fac;
       m = mx;
     }
-    const float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff - sc.off;
+    float ref = (m == -__builtin_inff() ? 0.0f : m) - kOff - sc.off;
+    if (fabsf(ref) > kFarMax) {
+      far_scores(sc, m, s);
+      ref = -kOff;
+    }
     // weights two at a time (pair j); a pair's arguments, exponentials and sum
     // are taken in three successive places
     u32x4_t p[2];
