@@ -182,7 +182,7 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   // over 6144 cached, 3 to a CU: 139 us, 2: 161, 4: 162, 6: 166.
   p.wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   const int d = c->head_dim;
-  const int per_cu = p.nt == 0 ? (d == 64 ? 4 : (d == 128 ? 2 + p.wide : 1))
+  const int per_cu = p.nt == 0 ? tile_waves(d, p.wide, x->softcap > kShortCap)
                                : (p.nt == 2 || d == 256 ? 2 : (d == 128 ? 3 : 4));
   p.want = cdiv(per_cu * (int64_t)num_cus(), c->heads);
   // One part, without the launch that joins several, as long as a wave has two
@@ -208,8 +208,12 @@ hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, hipStream_t st
   const unsigned grid = (unsigned)(p.places * a.c.heads);
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
-    e = p.wide ? launch(kv_tiled_kernel<MODE, D, true>, grid, kThreads, st, a)
-               : launch(kv_tiled_kernel<MODE, D, false>, grid, kThreads, st, a);
+    auto go = [&](auto cap) {
+      constexpr bool LONG = decltype(cap)::value;
+      return p.wide ? launch(kv_tiled_kernel<MODE, D, true, LONG>, grid, kThreads, st, a)
+                    : launch(kv_tiled_kernel<MODE, D, false, LONG>, grid, kThreads, st, a);
+    };
+    e = a.cap > kShortCap ? go(std::true_type{}) : go(std::false_type{});
   } else {
     auto go = [&](auto nt) {
       constexpr int N = decltype(nt)::value;

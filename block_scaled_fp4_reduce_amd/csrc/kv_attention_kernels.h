@@ -524,22 +524,62 @@ __device__ __forceinline__ float load_query(const AttnArgs& a, int h, const uint
 
 // Scores from the products x: in powers of two, s = f x + off with f > 0, so
 // that maxima can be taken of x and the weight is one fma and one exponential.
-// Capped ones, c tanh(s / c) = c - 2 c / (exp(2 s / c) + 1), have
-// x = -1 / (exp + 1) in place of the product, f = 2 c and off = c.
+//
+// Capped ones, c tanh(t) with t = s / c, have two forms:
+//  - caps up to kShortCap: c - 2 c / (exp(2 t) + 1), so x = -1 / (exp + 1)
+//    takes the place of the product, f = 2 c and off = c.  Its roundings are
+//    relative to c: 8 u c at most (u = 2^-24), 3e-5 of a weight at 64.
+//  - larger ones, whose scores lie around zero more often than not: x stays
+//    the product times tanh(t) / t, so the error follows the score.  Up to
+//    |t| = 0.3 that ratio is its series to t^8 (the first term left out is
+//    under u), beyond x = `top` (1 - 2 / (exp(2 t) + 1)), 16 u of the score.
+// Every score of the short form costs two transcendentals and two other
+// instructions, of the other one about nine more: a prompt of 8192 tokens with
+// a window of 4096 takes 481 us under a cap of 64 and 686 under one of 100,
+// chunks of 512 tokens over 6144 163 and 281, 64 decoding contexts 92 and 98.
+constexpr float kShortCap = 64.0f;
 struct ScoreScale {
-  float f, off, in;                      // in > 0: capped
+  float f, off, in;                      // in > 0: capped; 2 t in powers of two = in x
 };
 __device__ __forceinline__ ScoreScale score_scale(const AttnArgs& a, float qf) {
+  constexpr float kMax = 3.402823466e38f;
   ScoreScale s{qf, 0.0f, 0.0f};
   if (a.cap > 0.0f) {
-    s.in = qf * (2.0f / a.cap);          // a score in powers of two, s / c ln 2 of its tanh's
-    s.f = 2.0f * a.cap * kLog2e;
-    s.off = a.cap * kLog2e;
+    // finite for the least of caps, so that a product of 0 stays 0
+    s.in = fminf(qf * fminf(2.0f / a.cap, kMax), kMax);
+    if (a.cap <= kShortCap) {
+      s.f = fmaxf(2.0f * a.cap * kLog2e, 0x1p-126f);
+      s.off = a.cap * kLog2e;
+    }
   }
   return s;
 }
-__device__ __forceinline__ float capped(float x, float in) {
+__device__ __forceinline__ float capped_short(float x, float in) {
   return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x * in));
+}
+__device__ __forceinline__ float capped_long(float x, float in, float top) {
+  constexpr float k = 1.0f / (4.0f * kLog2e * kLog2e);           // t^2 = k y^2
+  const float y = x * in, z = y * y * k;
+  float r = __builtin_fmaf(z, 62.0f / 2835.0f, -17.0f / 315.0f);
+  r = __builtin_fmaf(z, r, 2.0f / 15.0f);
+  r = __builtin_fmaf(z, r, -1.0f / 3.0f);
+  r = __builtin_fmaf(z * r, x, x);
+  const float far = top * __builtin_fmaf(
+      -2.0f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y) + 1.0f), 1.0f);
+  return z < 0.09f ? r : far;
+}
+// A lane's capped scores (a vector of floats).
+template <bool LONG, typename V>
+__device__ __forceinline__ void cap_scores(const ScoreScale& sc, V& s) {
+  constexpr int N = sizeof(V) / sizeof(float);
+  if constexpr (LONG) {
+    const float top = fminf(2.0f * kLog2e / sc.in, 3.402823466e38f);       // c / f
+#pragma unroll
+    for (int r = 0; r < N; r++) s[r] = capped_long(s[r], sc.in, top);
+  } else {
+#pragma unroll
+    for (int r = 0; r < N; r++) s[r] = capped_short(s[r], sc.in);
+  }
 }
 
 // The weight of a score is exp2(f x - (m - off - kOff)) in one fma, whose exact
@@ -656,9 +696,10 @@ void kv_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < NT; i++)
 #pragma unroll
-        for (int t = 0; t < 4; t++)
-#pragma unroll
-          for (int r = 0; r < 4; r++) s[i][t][r] = capped(s[i][t][r], sc[i].in);
+        for (int t = 0; t < 4; t++) {
+          if (a.cap > kShortCap) cap_scores<true>(sc[i], s[i][t]);
+          else cap_scores<false>(sc[i], s[i][t]);
+        }
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // bytes of the tokens that count
     if (base < (uint32_t)lmax || base + kAttnKeys > (uint32_t)hmin || !__all(pg.v >= 0)) {

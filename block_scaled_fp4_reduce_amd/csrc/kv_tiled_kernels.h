@@ -152,8 +152,15 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-template <int MODE, int D, bool WIDE>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) void kv_tiled_kernel(AttnArgs a) {
+// Waves a SIMD, which are also the workgroups a CU.  LONG: capped scores above
+// kShortCap, in a kernel of its own, because their form takes registers that
+// the other calls' waves do not leave; it runs one wave less.
+constexpr int tile_waves(int dim, bool wide, bool lng) {
+  return dim == 64 ? 4 - lng : (dim == 128 ? 2 + (wide && !lng) : 1);
+}
+
+template <int MODE, int D, bool WIDE, bool LONG>
+__global__ __launch_bounds__(kThreads, tile_waves(D, WIDE, LONG)) void kv_tiled_kernel(AttnArgs a) {
   constexpr float kOff = MODE == 2 ? 0.0f : 12.0f, kLag = MODE == 2 ? 8.0f : 3.0f;
   constexpr int QS = D / 16, NT = D / 32;
   using L = TileLds<D>;
@@ -245,10 +252,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 2 + WIDE : 1)) 
       ok1 = v.y;
     }
     static_for<kAhead>([&](auto ii) { ring[decltype(ii)::value] = value_at(buf, decltype(ii)::value); });
-    if (a.cap > 0.0f) {
-#pragma unroll
-      for (int r = 0; r < 16; r++) s[r] = capped(s[r], sc.in);
-    }
+    if (LONG || a.cap > 0.0f) cap_scores<LONG>(sc, s);
     if (base < (uint32_t)wlmax || base + kTileKeys > (uint32_t)whmin || !(ok0 & ok1)) {
 #pragma unroll
       for (int r = 0; r < 16; r++) {

@@ -327,7 +327,9 @@ typedef struct {
                                   h reads kv head h / (q_heads / heads)       */
   int32_t window;              /* 0: none                                     */
   float scale;                 /* of the scores, usually head_dim^-1/2        */
-  float softcap;               /* c > 0: scores become c tanh(s / c); 0: none */
+  float softcap;               /* c > 0: scores become c tanh(s / c), off by
+                                  16 u of themselves and, up to c = 64, 8 u c
+                                  (u = 2^-24); 0: none                        */
 } fp4_kv_queries;
 
 /* Device workspace of fp4_kv_attention for these sizes (needs no
