@@ -90,7 +90,11 @@ template <int BYTE>
 __device__ __forceinline__ uint32_t fp4x2_bf16(uint32_t w, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, BYTE));
 }
-// E4M3 scale bytes 2 HI and 2 HI + 1 of w as fp16 (exact; the sign bit of a scale is not read).
+// The bits of four scale bytes that count: an E4M3 scale's sign is ignored, by
+// every decode of the library.
+template <int MODE>
+constexpr uint32_t kScaleBits = MODE == 2 ? 0xFFFFFFFFu : 0x7F7F7F7Fu;
+// E4M3 scale bytes 2 HI and 2 HI + 1 of w as fp16 (exact).
 template <bool HI>
 __device__ __forceinline__ f16x2_t e4m3x2_f16(uint32_t w) {
   return __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, HI));
@@ -424,7 +428,8 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, int h, uint32_t b
   }
 }
 
-// A operand of key rows: 8 channels of code dword `w` and the lane's scale.
+// A operand of key rows: 8 channels of code dword `w` and the lane's scales (of
+// kScaleBits).
 // IDX: position of the dword's scale among the lane's scale bytes.
 template <int MODE, int IDX>
 __device__ __forceinline__ u32x4_t key_operand(uint32_t w, uint32_t ks) {
@@ -447,7 +452,7 @@ __device__ __forceinline__ u32x4_t key_operand(uint32_t w, uint32_t ks) {
 }
 
 // A operands of the even and odd channels of a piece of the values: the
-// tokens of dwords w0, w1 with their scale bytes s0, s1.
+// tokens of dwords w0, w1 with their scale bytes s0, s1 (of kScaleBits).
 template <int MODE>
 __device__ __forceinline__ void value_operands(uint32_t w0, uint32_t w1, uint32_t s0, uint32_t s1,
                                                u32x4_t& even, u32x4_t& odd) {
@@ -686,7 +691,8 @@ void kv_attention_kernel(AttnArgs a) {
       constexpr int t = decltype(tt)::value;
       static_for<KD>([&](auto ss) {
         constexpr int st = decltype(ss)::value;
-        const u32x4_t k = key_operand<MODE, st * 8 / KeyFragment<MODE, D>::G>(kf.k[t][st], kf.s[t]);
+        const u32x4_t k = key_operand<MODE, st * 8 / KeyFragment<MODE, D>::G>(
+            kf.k[t][st], kf.s[t] & kScaleBits<MODE>);
 #pragma unroll
         for (int i = 0; i < NT; i++) s[i][t] = mfma16<MODE>(k, q[i][st], s[i][t]);
       });
@@ -701,7 +707,8 @@ void kv_attention_kernel(AttnArgs a) {
           else cap_scores<false>(sc[i], s[i][t]);
         }
     }
-    uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // bytes of the tokens that count
+    constexpr uint32_t kAll = kScaleBits<MODE>;
+    uint32_t keep[4] = {kAll, kAll, kAll, kAll};     // scale bits of the tokens that count
     if (base < (uint32_t)lmax || base + kAttnKeys > (uint32_t)hmin || !__all(pg.v >= 0)) {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
@@ -709,7 +716,7 @@ void kv_attention_kernel(AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; r++) {
           const int key = (int)base + 16 * g + 4 * t + r;
-          if (pg.v >= 0 && key >= lmin && key < hmax) keep[t] |= 255u << (8 * r);
+          if (pg.v >= 0 && key >= lmin && key < hmax) keep[t] |= kAll & 255u << (8 * r);
 #pragma unroll
           for (int i = 0; i < NT; i++)
             s[i][t][r] = pg.v < 0 || key < lo[i] || key >= hi[i] ? -__builtin_inff() : s[i][t][r];

@@ -98,11 +98,14 @@ struct TileLds {
   int ok[2][2];                          // narrow pages: that of each 16 tokens is in the cache
 };
 
-// Values of tokens outside [lo, hi) or without a page count as zeros: their
-// scales become zero.
+// The bits of the scales that count.  Values of tokens outside [lo, hi)
+// or without a page count as zeros: their scales become zero.
 template <int MODE, int D>
-__device__ __forceinline__ void drop_values(TileCodes<MODE, D>& f, uint32_t base, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ void clean_scales(TileCodes<MODE, D>& f, uint32_t base, uint32_t lo, uint32_t hi) {
   using C = TileCodes<MODE, D>;
+  f.ks &= kScaleBits<MODE>;
+#pragma unroll
+  for (int w = 0; w < C::W; w++) f.vs[w] &= kScaleBits<MODE>;
   if (base >= lo && base + kTileKeys <= hi && __all(f.vpage >= 0)) return;
   const int tok = ((int)threadIdx.x % C::TG) * C::TOK;
 #pragma unroll
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(kThreads, tile_waves(D, WIDE, LONG)) void kv_tiled_
       load_tile<MODE, D, WIDE>(a, h, base_of(i), kp, vp, f);
     };
     auto ready = [&](uint32_t i) {       // what the decode of tile i needs once
-      drop_values(f, base_of(i), tlo, thi);
+      clean_scales(f, base_of(i), tlo, thi);
       if constexpr (!WIDE)
         if (lane == 0) lds.ok[i & 1][wave >> 1] = f.kpage >= 0;  // 8 keys a wave
     };

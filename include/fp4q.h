@@ -279,7 +279,8 @@ int fp4_dequantize(int format, const uint8_t* codes, const uint8_t* scales,
  * Slot s is token s % P of page s / P.  Every head is quantized along
  * head_dim as nvfp4_quantize (flags FP4_RTN6 or FP4_FOUR_OVER_SIX, the
  * head's largest magnitude given as amax_in) or mxfp4_quantize would;
- * magnitudes past the given one saturate. */
+ * magnitudes past the given one saturate.  The sign bit of an E4M3 scale is
+ * ignored. */
 typedef struct {
   uint8_t* k_codes;
   uint8_t* k_scales;
