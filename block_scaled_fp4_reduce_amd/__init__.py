@@ -442,7 +442,7 @@ def fp4_kv_attention(cache, q, page_table, kv_lens, cu_q=None, max_q=0, scale=No
 
     q [tokens][q_heads][head_dim] bf16 holds the new tokens of all sequences
     one after another: sequence b's are cu_q[b] .. cu_q[b + 1] - 1 (int32;
-    None: one token each), the last of its kv_lens[b] cached ones (int32, the
+    None: one token each; tokens outside get zeros), the last of its kv_lens[b] cached ones (int32, the
     new ones written before).  page_table [seqs][width] (int32) names each
     sequence's pages.  max_q is the largest number of new tokens where the
     program knows it (0: not known).  Returns out (bf16, like q), or

@@ -251,9 +251,45 @@ __device__ __forceinline__ uint32_t item_of(const AttnArgs& a, uint32_t t, Work&
   return ~0u;
 }
 
+// Rows r0 .. r1 - 1 of head h, counted from token tok0 on, that see nothing.
+template <int D>
+__device__ __forceinline__ void clear_rows(const AttnArgs& a, int h, uint32_t tok0, uint32_t r0,
+                                           uint32_t r1) {
+  uint32_t group = (uint32_t)a.group;
+  asm volatile("" : "+s"(group));        // or its reciprocal stays in registers for good
+  for (uint32_t i = threadIdx.x; i < (r1 - r0) * (D / 8); i += blockDim.x) {
+    const uint32_t r = r0 + i / (D / 8), ch = i % (D / 8) * 8, tok = r / group;
+    const int64_t t = tok0 + tok;
+    const int head = (int)(h * group + (r - tok * group));
+    *(uint4*)(a.out + t * a.os + (int64_t)head * D + ch) = make_uint4(0, 0, 0, 0);
+    if (ch == 0 && a.lse) a.lse[t * a.hq + head] = -__builtin_inff();
+  }
+}
+
+// Tokens before the first sequence and past the last one see nothing.  The
+// tiles of the grid reach over them (tile_of: the first sequence's count back
+// to token 0, the last one's up to the last token), so each clears the rows
+// that no sequence has.  With parts the join does it.
+template <int D, uint32_t M>
+__device__ __forceinline__ void clear_gaps(const AttnArgs& a, int h, const Work& w, uint32_t next,
+                                           uint32_t t, uint32_t tile) {
+  const uint32_t group = (uint32_t)a.group;
+  if (w.b == 0 && w.tok0 > 0) {
+    const uint32_t end = w.tok0 * group;
+    if ((uint64_t)t * M < end) clear_rows<D>(a, h, 0, t * M, min(end, t * M + M));
+  }
+  if (w.b + 1 == (uint32_t)a.seqs && next < (uint32_t)a.tokens && next >= w.tok0) {
+    const uint32_t held = (next - w.tok0) * group, end = ((uint32_t)a.tokens - w.tok0) * group;
+    if ((uint64_t)tile * M < end) {
+      const uint32_t lo = max(held, tile * M), hi = min(end, tile * M + M);
+      if (lo < hi) clear_rows<D>(a, h, w.tok0, lo, hi);
+    }
+  }
+}
+
 // The work of place `t` for one head; false where there is none.
-template <uint32_t M>
-__device__ __forceinline__ bool find_work(const AttnArgs& a, uint32_t t, Work& w) {
+template <int D, uint32_t M>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int h, uint32_t t, Work& w) {
   uint32_t tile;
   if (a.splits > 1) {
     tile = item_of<M>(a, t, w);
@@ -269,6 +305,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, uint32_t t, Work& w
       w.tok0 = cu_at(a, w.b);
       const uint32_t next = cu_at(a, w.b + 1);
       w.n = next > w.tok0 ? (int)(next - w.tok0) : 0;
+      clear_gaps<D, M>(a, h, w, next, t, tile);
     }
     w.len = a.lens[w.b];
   }
@@ -621,7 +658,7 @@ void kv_attention_kernel(AttnArgs a) {
   const uint32_t place = blockIdx.x / (uint32_t)a.c.heads;
   const int h = (int)(blockIdx.x - place * (uint32_t)a.c.heads);
   Work rt;
-  if (!find_work<M>(a, place, rt)) return;
+  if (!find_work<D, M>(a, h, place, rt)) return;
   const int split = (int)rt.split;
   // reach of the tile's rows: [lo, hi) of each column, and of all together
   const uint32_t group = (uint32_t)a.group;
@@ -892,7 +929,11 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(AttnArgs a,
   if (live) {
     // with few rows the loads do not wait for the number of parts (sums that
     // were not written are read and dropped): the call is all latency
-    const int n = a.parts[row], most = eager ? a.splits : n;
+    // Rows of no sequence have no number of parts: theirs is whatever the
+    // workspace held.
+    const uint32_t at = (uint32_t)row / (uint32_t)a.hq;
+    const bool held = !a.cu || (at >= cu_at(a, 0) && at < cu_at(a, (uint32_t)a.seqs));
+    const int n = held ? min(max(a.parts[row], 0), a.splits) : 0, most = eager ? a.splits : n;
     for (int s0 = grp; s0 < most; s0 += 4 * groups) {
       float2 ml[4];
       float4 y[4];

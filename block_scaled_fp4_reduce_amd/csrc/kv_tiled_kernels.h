@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads, tile_waves(D, WIDE, LONG)) void kv_tiled_
   const uint32_t place = blockIdx.x / (uint32_t)a.c.heads;
   const int h = (int)(blockIdx.x - place * (uint32_t)a.c.heads);
   Work rt;
-  if (!find_work<kTileRows>(a, gridDim.x / (uint32_t)a.c.heads - 1 - place, rt)) return;
+  if (!find_work<D, kTileRows>(a, h, gridDim.x / (uint32_t)a.c.heads - 1 - place, rt)) return;
   const int split = (int)rt.split;
   const uint32_t group = (uint32_t)a.group;
   auto hi_of = [&](uint32_t row) {

@@ -317,8 +317,11 @@ typedef struct {
   int64_t q_stride;
   int64_t tokens;              /* new tokens of all sequences                 */
   int64_t seqs;
-  const int32_t* cu_q;         /* [seqs + 1] first token of each sequence,
-                                  cu_q[seqs] = tokens; NULL: one token each   */
+  const int32_t* cu_q;         /* [seqs + 1] first token of each sequence and
+                                  the end of the last, none less than the one
+                                  before; tokens before cu_q[0] and from
+                                  cu_q[seqs] on (a padded batch) belong to no
+                                  sequence.  NULL: one token each             */
   int64_t max_q;               /* at least every sequence's number of new
                                   tokens; 0: not known                        */
   const int32_t* kv_lens;      /* [seqs] cached tokens, the new ones included */
@@ -340,8 +343,8 @@ size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_
 /* out = softmax(scores) V over the cached tokens that each new token sees,
  * bf16 [tokens][q_heads][head_dim]; lse NULL or [tokens][q_heads] floats,
  * the log of the sum of the scores' exponentials.  A token that sees
- * nothing (kv_len 0, or fewer cached tokens than new ones) gets out = 0 and
- * lse = -inf.  Cached bytes past a sequence's length are never looked at,
+ * nothing (kv_len 0, fewer cached tokens than new ones, or no sequence) gets
+ * out = 0 and lse = -inf.  Cached bytes past a sequence's length are never looked at,
  * whatever they hold; a page id outside the cache contributes nothing; a
  * length past the table is cut to it.  out may not overlap q; tokens times
  * q_heads, and sequences times q_heads, stay below 2^31.  Equal calls give
