@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPCachingAllocator.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -114,10 +115,16 @@ struct Stream {
   }
   Stream(PyObject* o, const at::Tensor& on)
       : guard(on.device()), stream(of(o, on.device())), given(o != Py_None) {}
-  // New tensors belong to the current stream; work on another holds them back from reuse.
+  // New tensors come from the memory of the stream that writes them: what
+  // another stream freed may still be in use there.  The caller's current
+  // stream, which reads them later, holds them back from reuse.
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& on) {
-    at::Tensor t = at::empty(shape, on.options().dtype(type));
-    if (given && t.numel()) c10::hip::HIPCachingAllocator::recordStream(t.storage().data_ptr(), stream);
+    const at::TensorOptions options = on.options().dtype(type);
+    const c10::hip::HIPStream current = c10::hip::getCurrentHIPStream(stream.device_index());
+    if (!given || stream == current) return at::empty(shape, options);
+    const c10::hip::HIPStreamGuard there(stream);
+    at::Tensor t = at::empty(shape, options);
+    if (t.numel()) c10::hip::HIPCachingAllocator::recordStream(t.storage().data_ptr(), current);
     return t;
   }
   void* raw() { return (void*)stream.stream(); }
