@@ -374,7 +374,9 @@ def _ints(x, dtype, shape, what):
 class KvCache:
     """A paged FP4 cache of keys and values: the buffers of ``fp4_kv_cache``
     (include/fp4q.h) and what their bytes mean.  ``alloc`` makes the buffers;
-    the constructor takes a program's own."""
+    the constructor takes a program's own.  The fields are fixed, since the
+    calls use the addresses taken here: other buffers or maxima need another
+    handle, or are copied into these tensors."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_amax", "v_amax", "fmt", "flags",
                  "pages", "heads", "page_size", "head_dim", "_c", "_at")
@@ -394,14 +396,22 @@ class KvCache:
                 if t is None:
                     raise ValueError("NVFP4 needs %s [heads]" % what)
                 _ints(t, torch.float32, (heads,), what)
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
-                                                                    v_scales)
-        self.k_amax, self.v_amax, self.fmt, self.flags = k_amax, v_amax, fmt, flags
-        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, dim
-        self._c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                          v_scales.data_ptr(), _ptr(k_amax), _ptr(v_amax), pages, page_size, heads,
-                          dim, fmt, flags)
-        self._at = C.addressof(self._c)
+        c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                    v_scales.data_ptr(), _ptr(k_amax), _ptr(v_amax), pages, page_size, heads, dim,
+                    fmt, flags)
+        for name, value in zip(self.__slots__, (k_codes, k_scales, v_codes, v_scales, k_amax, v_amax,
+                                                fmt, flags, pages, heads, page_size, dim, c,
+                                                C.addressof(c))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("the fields of a cache handle are fixed: %s" % name)
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def __copy__(self):
+        return self
 
     @classmethod
     def alloc(cls, pages, page_size, heads, head_dim, fmt=FORMAT_NVFP4, flags=0, k_amax=None,
