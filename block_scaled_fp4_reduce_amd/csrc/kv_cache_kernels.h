@@ -42,8 +42,11 @@ __device__ __forceinline__ void kv_quant32(const float* y, uint32_t* w, uint32_t
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; i++) m = fmaxf(m, fabsf(y[i]));
+  // Up to 252, the scale of the largest finite values: with an infinity's 253 the
+  // largest code reads as infinity, and in attention 0 times that is NaN for the
+  // rows that give the token no weight.
   const int ef = (int)(__float_as_uint(m) >> 23);
-  scale = (uint32_t)(ef > 2 ? ef - 2 : 0);
+  scale = (uint32_t)(ef > 2 ? min(ef - 2, 252) : 0);
   const float s = __uint_as_float(scale << 23);
 #pragma unroll
   for (int i = 0; i < 4; i++) {

@@ -280,7 +280,9 @@ int fp4_dequantize(int format, const uint8_t* codes, const uint8_t* scales,
  * head_dim as nvfp4_quantize (flags FP4_RTN6 or FP4_FOUR_OVER_SIX, the
  * head's largest magnitude given as amax_in) or mxfp4_quantize would;
  * magnitudes past the given one saturate.  The sign bit of an E4M3 scale is
- * ignored. */
+ * ignored.  An infinity is stored as the largest value, a NaN as some finite
+ * one, so either reaches only the tokens that see it.  In a program's own bytes
+ * the E4M3 code 0x7F and UE8M0 codes above 252 are outside the domain. */
 typedef struct {
   uint8_t* k_codes;
   uint8_t* k_scales;
