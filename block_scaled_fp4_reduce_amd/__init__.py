@@ -478,9 +478,51 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, table, eps=1e-6, interleav
     its weight ([head_dim] bf16; None: no norm), then the rotation of the
     first 2 * table.shape[1] values by the angles of ``positions`` [tokens]
     (int64) in ``table`` (``rope_table``).  Returns (q, k); ``out`` may supply
-    them and may be (q, k) themselves."""
+    them and may be (q, k) themselves.  Where q, k or a weight requires a
+    gradient (and grad mode is on) the results carry it through torch's
+    autograd, by ``qk_norm_rope_backward``; ``out`` is refused then.  A capture
+    of such a backward needs what torch asks of any: no graph of the same
+    leaves from outside the capture is alive."""
     return _binding().norm_rope(q, k, q_weight, k_weight, positions, table, eps, interleaved, out,
                                 stream)
+
+
+_norm_rope_function = None
+
+
+def _rows(g):
+    """g [tokens][heads][head_dim] laid out as the calls take it."""
+    tokens, heads, dim = g.shape
+    fits = (g.stride()[1:] == (dim, 1) and g.stride(0) >= heads * dim and g.stride(0) % 8 == 0 and
+            g.data_ptr() % 16 == 0)
+    return g if fits else g.clone(memory_format=_torch().contiguous_format)
+
+
+def _norm_rope_autograd(*args):
+    """qk_norm_rope(q, k, q_weight, k_weight, positions, table, eps, interleaved,
+    stream) as a node of torch's autograd graph."""
+    global _norm_rope_function
+    if _norm_rope_function is None:
+        torch = _torch()
+
+        class NormRope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_weight, k_weight, positions, table, eps, interleaved, stream):
+                ctx.save_for_backward(q, k, q_weight, k_weight, positions, table)
+                ctx.how = eps, interleaved
+                return qk_norm_rope(q, k, q_weight, k_weight, positions, table, eps, interleaved,
+                                    stream=stream)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dq_out, dk_out):
+                x = ctx.saved_tensors
+                grads = qk_norm_rope_backward(_rows(dq_out), _rows(dk_out), *x, *ctx.how)
+                return tuple(None if g is None or not need else g.to(torch.bfloat16)
+                             for g, need in zip(grads, ctx.needs_input_grad)) + (None,) * 5
+
+        _norm_rope_function = NormRope
+    return _norm_rope_function.apply(*args)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, table, eps=1e-6,

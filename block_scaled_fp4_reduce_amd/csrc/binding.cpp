@@ -5,12 +5,14 @@
 // the norm of one decoding batch takes 5.5 us a call (17.3 through ctypes and torch.empty).
 //
 // Errors: TypeError for a wrong dtype, ValueError for a wrong shape, layout or
-// device, Fp4Error for a status of the library.
+// device, Fp4Error for a status of the library, RuntimeError where a gradient
+// would be lost.
 #include <Python.h>
 
 #include <string>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPCachingAllocator.h>
@@ -301,15 +303,42 @@ Heads like(const at::Tensor& t, const fp4_qk_rope& x, int64_t heads, const char*
   return h;
 }
 
-// norm_rope([rope], out, stream) -> (q, k)
+bool wants_gradient(PyObject* const* a, int n) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (int i = 0; i < n; i++)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+  return false;
+}
+
+// A function of the package, called with n positional arguments.
+PyObject* in_package(const char* name, PyObject* const* a, int n) {
+  PyObject* m = PyImport_ImportModule("block_scaled_fp4_reduce_amd");
+  PyObject* f = m ? PyObject_GetAttrString(m, name) : nullptr;
+  PyObject* r = f ? PyObject_Vectorcall(f, a, n, nullptr) : nullptr;
+  Py_XDECREF(f);
+  Py_XDECREF(m);
+  if (!r) throw PyError{};
+  return r;
+}
+
+// norm_rope([rope], out, stream) -> (q, k); by way of torch's autograd where
+// an input wants a gradient
 PyObject* norm_rope(PyObject* const* a) {
+  PyObject* given[2];
+  pair_of(a[8], &given[0], &given[1]);
+  if (wants_gradient(a, 6) || wants_gradient(given, 2)) {
+    if (wants_gradient(a + 5, 1))
+      fail(PyExc_RuntimeError, "qk_norm_rope has no gradient of its table");
+    if (a[8] != Py_None)
+      fail(PyExc_RuntimeError, "qk_norm_rope: out cannot carry the gradient that an input requires");
+    PyObject* const args[] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[9]};
+    return in_package("_norm_rope_autograd", args, 9);
+  }
   const fp4_qk_rope x = rope_of(a);
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
-  PyObject *oq, *ok;
-  pair_of(a[8], &oq, &ok);
   Stream st(a[9], q);
-  const at::Tensor yq = given_or_new(oq, "out q", st, q.sizes(), at::kBFloat16, q);
-  const at::Tensor yk = given_or_new(ok, "out k", st, k.sizes(), at::kBFloat16, k);
+  const at::Tensor yq = given_or_new(given[0], "out q", st, q.sizes(), at::kBFloat16, q);
+  const at::Tensor yk = given_or_new(given[1], "out k", st, k.sizes(), at::kBFloat16, k);
   const Heads hq = like(yq, x, x.q_heads, "out q"), hk = like(yk, x, x.k_heads, "out k");
   check("qk_norm_rope", qk_norm_rope(&x, hq.p, hq.stride, hk.p, hk.stride, st.raw()));
   return pair(yq, yk);
