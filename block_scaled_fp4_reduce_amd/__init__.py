@@ -429,7 +429,8 @@ class KvCache:
 def fp4_kv_write(cache, k, v, slots, stream=None):
     """Quantize keys and values [tokens][heads][head_dim] (bf16) into ``cache``
     at ``slots`` [tokens] (int64; slot s is token s % page_size of page
-    s / page_size).  Slots outside the cache are skipped."""
+    s / page_size).  Slots outside the cache are skipped.  What is stored are
+    bytes, through which no gradient goes."""
     _binding().kv_write(cache._at, k, v, slots, stream)
 
 
@@ -455,8 +456,10 @@ def fp4_kv_attention(cache, q, page_table, kv_lens, cu_q=None, max_q=0, scale=No
     None: one token each; tokens outside get zeros), the last of its kv_lens[b] cached ones (int32, the
     new ones written before).  page_table [seqs][width] (int32) names each
     sequence's pages.  max_q is the largest number of new tokens where the
-    program knows it (0: not known).  Returns out (bf16, like q), or
-    (out, lse) with lse [tokens][q_heads] float32."""
+    program knows it (0: not known).  Scores beyond `softcap` c > 0 level off,
+    c tanh(s / c).  Returns out (bf16, like q), or (out, lse) with lse
+    [tokens][q_heads] float32.  There is no backward: queries that require a
+    gradient are refused in grad mode."""
     return _binding().kv_attention(cache._at, q, page_table, kv_lens, cu_q, max_q, scale, softcap,
                                    window, want_lse, out, lse, ws, stream)
 

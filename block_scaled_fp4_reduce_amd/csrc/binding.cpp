@@ -144,6 +144,14 @@ void check(const char* fn, int status) {
   throw PyError{};
 }
 
+// Whether one of the tensors among a[0 .. n - 1] requires a gradient, in grad mode.
+bool wants_gradient(PyObject* const* a, int n) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (int i = 0; i < n; i++)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+  return false;
+}
+
 // The caller's tensor, or a new one.
 at::Tensor given_or_new(PyObject* o, const char* what, Stream& st, at::IntArrayRef shape,
                         at::ScalarType type, const at::Tensor& on) {
@@ -236,6 +244,10 @@ PyObject* kv_attention_ws(PyObject* const* a) {
 
 // kv_attention(cache, [queries], want_lse, out, lse, ws, stream) -> out or (out, lse)
 PyObject* kv_attention(PyObject* const* a) {
+  PyObject* const floats[] = {a[1], a[10], a[11]};
+  if (wants_gradient(floats, 3))
+    fail(PyExc_RuntimeError, "fp4_kv_attention has no backward, but a tensor requires a gradient: "
+                             "detach it or call under torch.no_grad()");
   const fp4_kv_cache* c = cache_of(a[0]);
   const fp4_kv_queries x = queries_of(c, a + 1);
   const at::Tensor& q = tensor(a[1], "q");
@@ -301,13 +313,6 @@ Heads like(const at::Tensor& t, const fp4_qk_rope& x, int64_t heads, const char*
   const Heads h = heads_of(t, heads, x.head_dim, what);
   if (h.tokens != x.tokens) fail(PyExc_ValueError, std::string(what) + " has another number of tokens");
   return h;
-}
-
-bool wants_gradient(PyObject* const* a, int n) {
-  if (!at::GradMode::is_enabled()) return false;
-  for (int i = 0; i < n; i++)
-    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
-  return false;
 }
 
 // A function of the package, called with n positional arguments.

@@ -50,3 +50,26 @@ def test_other_refusals_come_through_autograd():
         fp4.qk_norm_rope(bf(3, 2, 64, grad=True), bf(3, 1, 64), None, None, *REST)
     with pytest.raises(TypeError):
         fp4.qk_norm_rope(bf(3, 2, 64, grad=True).float(), bf(3, 1, 64), None, None, *REST)
+
+
+class Handle:
+    """A cache handle that was never allocated: only its numbers are read."""
+
+    def __init__(self):
+        p = 0x10000
+        self._c = fp4._CCache(p, p, p, p, p, p, 4, 16, 2, 64, fp4.FORMAT_NVFP4, 0)
+        self._at = fp4.C.addressof(self._c)
+
+
+def test_attention_refuses_queries_that_require_gradients():
+    args = torch.zeros(3, 1, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    q = bf(3, 4, 64, grad=True)
+    with pytest.raises(RuntimeError, match="no backward"):
+        fp4.fp4_kv_attention(Handle(), q, *args)
+    with pytest.raises(RuntimeError, match="no backward"):
+        fp4.fp4_kv_attention(Handle(), q.detach(), *args, out=q)
+    for x in (q.detach(), bf(3, 4, 64)):
+        with pytest.raises(ValueError):                      # host tensors
+            fp4.fp4_kv_attention(Handle(), x, *args)
+    with torch.no_grad(), pytest.raises(ValueError):
+        fp4.fp4_kv_attention(Handle(), q, *args)
