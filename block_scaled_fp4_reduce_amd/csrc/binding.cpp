@@ -152,10 +152,13 @@ bool wants_gradient(PyObject* const* a, int n) {
   return false;
 }
 
-// The caller's tensor, or a new one.
+// The caller's tensor, which counts as modified from here on, or a new one.
 at::Tensor given_or_new(PyObject* o, const char* what, Stream& st, at::IntArrayRef shape,
                         at::ScalarType type, const at::Tensor& on) {
-  return o == Py_None ? st.empty(shape, type, on) : tensor(o, what);
+  if (o == Py_None) return st.empty(shape, type, on);
+  const at::Tensor& t = tensor(o, what);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return t;
 }
 
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
@@ -258,7 +261,7 @@ PyObject* kv_attention(PyObject* const* a) {
   at::Tensor lse;
   if (a[11] != Py_None) {
     array_of<float>(a[11], at::kFloat, {x.tokens, x.q_heads}, "lse");
-    lse = tensor(a[11], "lse");
+    lse = given_or_new(a[11], "lse", st, {}, at::kFloat, q);
   } else if (truth(a[9])) {
     lse = st.empty({x.tokens, x.q_heads}, at::kFloat, q);
   }
