@@ -371,6 +371,15 @@ def _ints(x, dtype, shape, what):
     return x.data_ptr()
 
 
+class _Address(int):
+    """The address of a handle's struct, with the device of its buffers."""
+
+    def __new__(cls, struct, device_index):
+        at = super().__new__(cls, C.addressof(struct))
+        at.device_index = device_index
+        return at
+
+
 class KvCache:
     """A paged FP4 cache of keys and values: the buffers of ``fp4_kv_cache``
     (include/fp4q.h) and what their bytes mean.  ``alloc`` makes the buffers;
@@ -396,12 +405,16 @@ class KvCache:
                 if t is None:
                     raise ValueError("NVFP4 needs %s [heads]" % what)
                 _ints(t, torch.float32, (heads,), what)
+        for t in (k_scales, v_codes, v_scales, k_amax, v_amax):
+            if t is not None and t.device != k_codes.device:
+                raise ValueError("the cache's tensors are on different devices: %s and %s" % (
+                    k_codes.device, t.device))
         c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                     v_scales.data_ptr(), _ptr(k_amax), _ptr(v_amax), pages, page_size, heads, dim,
                     fmt, flags)
         for name, value in zip(self.__slots__, (k_codes, k_scales, v_codes, v_scales, k_amax, v_amax,
                                                 fmt, flags, pages, heads, page_size, dim, c,
-                                                C.addressof(c))):
+                                                _Address(c, k_codes.device.index))):
             object.__setattr__(self, name, value)
 
     def __setattr__(self, name, value):

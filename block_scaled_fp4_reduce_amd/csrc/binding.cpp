@@ -179,15 +179,44 @@ void pair_of(PyObject* o, PyObject** a, PyObject** b) {
   *b = PySequence_Fast_GET_ITEM(o, 1);
 }
 
+// The kernels of a call run on one device, on memory of that device: its tensors
+// among a[0 .. n - 1], and those of the cache (an index, -1: not known).
+void one_device(PyObject* const* a, int n, int64_t cache = -1) {
+  const at::Tensor* first = nullptr;
+  for (int i = 0; i < n; i++) {
+    if (!THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (!first) first = &t;
+    if (t.device() != first->device())
+      fail(PyExc_ValueError, "tensors of one call on different devices: " + first->device().str() +
+                                 " and " + t.device().str());
+  }
+  if (first && cache >= 0 && first->is_cuda() && first->device().index() != cache)
+    fail(PyExc_ValueError, "the cache is on another device (cuda:" + std::to_string(cache) +
+                               ") than the tensors: " + first->device().str());
+}
+
+// The handle's own struct, from its address; and the device that an address
+// knows.
 const fp4_kv_cache* cache_of(PyObject* o) {
-  void* p = PyLong_AsVoidPtr(o);         // the address of the handle's own struct
+  void* p = PyLong_AsVoidPtr(o);
   if (!p) throw PyError{};
   return (const fp4_kv_cache*)p;
+}
+int64_t device_of(PyObject* o) {
+  if (PyLong_CheckExact(o)) return -1;
+  PyObject* d = PyObject_GetAttrString(o, "device_index");
+  if (!d) throw PyError{};
+  const int64_t i = PyLong_AsLongLong(d);
+  Py_DECREF(d);
+  if (i == -1 && PyErr_Occurred()) throw PyError{};
+  return i;
 }
 
 // kv_write(cache, k, v, slots, stream)
 PyObject* kv_write(PyObject* const* a) {
   const fp4_kv_cache* c = cache_of(a[0]);
+  one_device(a + 1, 3, device_of(a[0]));
   const Heads k = heads_of(a[1], c->heads, c->head_dim, "k"), v = heads_of(a[2], c->heads, c->head_dim, "v");
   if (v.tokens != k.tokens) fail(PyExc_ValueError, "k and v disagree on the number of tokens");
   const int64_t* slots = array_of<int64_t>(a[3], at::kLong, {k.tokens}, "slots");
@@ -201,12 +230,13 @@ PyObject* kv_read(PyObject* const* a) {
   const fp4_kv_cache* c = cache_of(a[0]);
   const at::Tensor& s = tensor(a[1], "slots");
   const int64_t n = s.dim() ? s.size(0) : 0;
+  PyObject* all[] = {a[1], nullptr, nullptr};
+  pair_of(a[2], &all[1], &all[2]);
+  one_device(all, 3, device_of(a[0]));
   const int64_t* slots = array_of<int64_t>(a[1], at::kLong, {n}, "slots");
-  PyObject *ok, *ov;
-  pair_of(a[2], &ok, &ov);
   Stream st(a[3], s);
-  const at::Tensor k = given_or_new(ok, "k", st, {n, c->heads, c->head_dim}, at::kBFloat16, s);
-  const at::Tensor v = given_or_new(ov, "v", st, {n, c->heads, c->head_dim}, at::kBFloat16, s);
+  const at::Tensor k = given_or_new(all[1], "k", st, {n, c->heads, c->head_dim}, at::kBFloat16, s);
+  const at::Tensor v = given_or_new(all[2], "v", st, {n, c->heads, c->head_dim}, at::kBFloat16, s);
   const Heads hk = heads_of(k, c->heads, c->head_dim, "k"), hv = heads_of(v, c->heads, c->head_dim, "v");
   if (hk.tokens != n || hv.tokens != n)
     fail(PyExc_ValueError, "k, v and slots disagree on the number of tokens");
@@ -240,6 +270,7 @@ fp4_kv_queries queries_of(const fp4_kv_cache* c, PyObject* const* a) {
 // kv_attention_ws(cache, [queries]) -> bytes
 PyObject* kv_attention_ws(PyObject* const* a) {
   const fp4_kv_cache* c = cache_of(a[0]);
+  one_device(a + 1, 4, device_of(a[0]));
   const fp4_kv_queries x = queries_of(c, a + 1);
   c10::DeviceGuard guard(tensor(a[1], "q").device());
   return PyLong_FromSize_t(fp4_kv_attention_workspace_bytes(c, &x));
@@ -252,6 +283,8 @@ PyObject* kv_attention(PyObject* const* a) {
     fail(PyExc_RuntimeError, "fp4_kv_attention has no backward, but a tensor requires a gradient: "
                              "detach it or call under torch.no_grad()");
   const fp4_kv_cache* c = cache_of(a[0]);
+  PyObject* const all[] = {a[1], a[2], a[3], a[4], a[10], a[11], a[12]};
+  one_device(all, 7, device_of(a[0]));
   const fp4_kv_queries x = queries_of(c, a + 1);
   const at::Tensor& q = tensor(a[1], "q");
   Stream st(a[13], q);
@@ -342,6 +375,8 @@ PyObject* norm_rope(PyObject* const* a) {
     PyObject* const args[] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[9]};
     return in_package("_norm_rope_autograd", args, 9);
   }
+  PyObject* const all[] = {a[0], a[1], a[2], a[3], a[4], a[5], given[0], given[1]};
+  one_device(all, 8);
   const fp4_qk_rope x = rope_of(a);
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
   Stream st(a[9], q);
@@ -354,15 +389,17 @@ PyObject* norm_rope(PyObject* const* a) {
 
 // norm_rope_backward(dq_out, dk_out, [rope], out, ws, stream) -> (dq, dk, dq_weight, dk_weight)
 PyObject* norm_rope_backward(PyObject* const* a) {
+  PyObject* given[2];
+  pair_of(a[10], &given[0], &given[1]);
+  PyObject* const all[] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[11], given[0], given[1]};
+  one_device(all, 11);
   const fp4_qk_rope x = rope_of(a + 2);
   const at::Tensor &q = tensor(a[2], "q"), &k = tensor(a[3], "k");
   const Heads gq = like(tensor(a[0], "dq_out"), x, x.q_heads, "dq_out");
   const Heads gk = like(tensor(a[1], "dk_out"), x, x.k_heads, "dk_out");
-  PyObject *oq, *ok;
-  pair_of(a[10], &oq, &ok);
   Stream st(a[12], q);
-  const at::Tensor dq = given_or_new(oq, "out dq", st, q.sizes(), at::kBFloat16, q);
-  const at::Tensor dk = given_or_new(ok, "out dk", st, k.sizes(), at::kBFloat16, k);
+  const at::Tensor dq = given_or_new(given[0], "out dq", st, q.sizes(), at::kBFloat16, q);
+  const at::Tensor dk = given_or_new(given[1], "out dk", st, k.sizes(), at::kBFloat16, k);
   const Heads hq = like(dq, x, x.q_heads, "out dq"), hk = like(dk, x, x.k_heads, "out dk");
   at::Tensor dqw, dkw, ws;
   if (x.q_weight) dqw = st.empty({x.head_dim}, at::kFloat, q);
