@@ -47,6 +47,31 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// v <- n = v r of one head.  Returns r.  Where the squares leave the range of
+// fp32 (values past 2^60; with an eps below 2^-90 also small ones) the head is
+// scaled by a power of two first; r itself may then be a subnormal.
+template <int LPH>
+__device__ __forceinline__ float norm_head(float* v, const RopeArgs& a) {
+  float ss = 0.0f, c = 1.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) ss = __builtin_fmaf(v[i], v[i], ss);
+  ss = group_sum<LPH>(ss) / (float)a.dim + a.eps;
+  if (!(ss >= 0x1p-90f && ss <= 3.402823466e38f)) {
+    c = ss < 1.0f ? 0x1p100f : 0x1p-80f;
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      v[i] *= c;
+      ss = __builtin_fmaf(v[i], v[i], ss);
+    }
+    ss = group_sum<LPH>(ss) / (float)a.dim + a.eps * c * c;
+  }
+  const float r = 1.0f / sqrtf(ss);
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] *= r;
+  return r * c;
+}
+
 // One lane's cosines and sines: its 8 values' pairs (half-split), or its 4
 // pairs (interleaved).
 template <bool INTER>
@@ -153,12 +178,9 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_kernel(RopeArgs a, 
     unpack8(raw, v);
     if (h < a.hq ? a.qw != nullptr : a.kw != nullptr) {
       unpack8(h < a.hq ? wq : wk, w);
-      float ss = 0.0f;
+      norm_head<LPH>(v, a);
 #pragma unroll
-      for (int i = 0; i < 8; i++) ss = __builtin_fmaf(v[i], v[i], ss);
-      const float r = 1.0f / sqrtf(group_sum<LPH>(ss) / (float)a.dim + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = v[i] * r * w[i];
+      for (int i = 0; i < 8; i++) v[i] *= w[i];
     }
     turn.template apply<false>(v);
     uint16_t* y = (h < a.hq ? qo : ko) + head_off(a, tok, h, qos, kos);
@@ -212,14 +234,10 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_bwd_kernel(
       if (isq ? a.qw != nullptr : a.kw != nullptr) {
         unpack8(rx, x);
         unpack8(isq ? wq : wk, w);
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) ss = __builtin_fmaf(x[i], x[i], ss);
-        const float r = 1.0f / sqrtf(group_sum<LPH>(ss) / (float)a.dim + a.eps);
+        const float r = norm_head<LPH>(x, a);         // x is n now
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          x[i] *= r;                                  // n
           const float t = g[i] * x[i];
           gq[i] += isq ? t : 0.0f;
           gk[i] += isq ? 0.0f : t;
