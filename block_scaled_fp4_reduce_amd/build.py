@@ -41,8 +41,12 @@ def deps():
 
 
 def binding_command(out):
-    """g++ command of the binding, linked to the libfp4q.so beside it."""
-    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """g++ command of the binding, linked to the libfp4q.so beside it; None
+    without torch, which the C library does not need."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    root = torch.submodule_search_locations[0]
     inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
            "/opt/rocm/include", sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
@@ -72,6 +76,10 @@ def build(verbose: bool = False) -> str:
         subprocess.check_call(link)
         os.replace(tmp, LIB)
         cmd = binding_command(tmp)       # links to the library, so it comes after
+        if cmd is None:
+            print("torch is not installed: libfp4q.so is built without the Python binding _calls.so",
+                  flush=True)
+            return LIB
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
