@@ -177,9 +177,10 @@ AttnPlan attention_plan(const fp4_kv_cache* c, const fp4_kv_queries* x) {
   const int64_t blocks = cdiv(keys, kAttnKeys);
   // Workgroups wanted per kv head.  How they are shared out among the
   // sequences depends on lengths that only the device knows (item_of); a
-  // tile gets at most four times an even share.  As many as run at once (by
-  // their registers), so that all of them end together: chunks of 512 tokens
-  // over 6144 cached, 3 to a CU: 139 us, 2: 161, 4: 162, 6: 166.
+  // tile gets at most four times an even share.  As many as run at once, so
+  // that all of them end together: chunks of 512 tokens over 6144 cached, heads
+  // of 128, 3 to a CU: 139 us, 2: 161, 4: 162, 6: 166.  (Two column tiles of
+  // heads of 64 would run 3 by their registers and are counted as 2.)
   p.wide = c->page_size >= (p.nt == 0 ? kTileKeys : kAttnKeys);
   const int d = c->head_dim;
   const int per_cu = p.nt == 0 ? tile_waves(d, p.wide, x->softcap > kShortCap)

@@ -24,7 +24,8 @@
 // The weights are rounded to the operand's type, to half a step of 2^-10
 // (fp16) or 2^-7 (bf16) of each: the sum over the row uses the unrounded
 // ones, and the accumulators are fp32.  fp16 weights carry a factor 2^12,
-// so that only those under 2^-26 of the largest lose bits.
+// so that only those under 2^-26 of the largest lose bits (a step is 2^-36 of
+// it there).
 //
 // The kernel here is for few rows (up to 32 a sequence and kv head; the tiled
 // one takes more): a wave decodes 64 keys and values straight into its operand
@@ -35,8 +36,8 @@
 // sequences of 2048 to 8192 tokens (8 kv heads, NVFP4 4/6, 379 MB) in 93 us
 // of calls, 4.1 TB/s, where a large copy moves 4.85; 2 sequences up to 131072
 // (MXFP4, 219 MB) in 53 us.  Vector instructions issue in 46% of the cycles.
-// Short contexts are all latency: 2048 tokens of one sequence 7.2 us and 3.1
-// to 3.9 for the join, in 10.1 us a call.
+// Short contexts are all latency: 2048 tokens of one sequence 7.3 us and 3.1
+// to 4.1 for the join, in 10.4 us a call.
 #pragma once
 
 #include "kv_common.h"

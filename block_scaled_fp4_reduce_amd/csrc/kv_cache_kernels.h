@@ -70,8 +70,10 @@ constexpr int kv_group() { return MODE == 2 ? 32 : 16; }
 //
 // Memory bounds the long calls: 65536 tokens of 8 heads of 128 (NVFP4 4/6, 344
 // MB) read in 71 to 73 us, 4.7 TB/s, where a large copy moves 4.85.  8192
-// tokens written take 13 to 15 us (43 MB; the arithmetic of both 4/6
-// candidates is about half of it) and 8.4 to 9.5 us read.  One lane per group
+// tokens written take 13 to 15 us (43 MB: 8.9 us at that rate; vector
+// instructions issue in 47% of the dispatch's cycles, and a wave waits to issue
+// for 46% of its time and for data for 34%) and 8.4 to 9.8 us read (27%, 30%
+// and 49%).  One lane per group
 // with byte loads and stores for the values took 169 us and 46 for the pair.
 // A decoding step's 256 scattered tokens take 5.8 and 6.2 us, all latency.
 //

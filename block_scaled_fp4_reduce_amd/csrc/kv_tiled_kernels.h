@@ -13,12 +13,15 @@
 // products of the first half's values (double buffers, one barrier per tile).
 // Tiles of 32 keys keep the registers of a wave at 168, so that three run on
 // a SIMD.  Vector instructions bound it: counted at D = 128, MXFP4, capped,
-// they issue in 74% of the cycles and the matrix unit runs in 36%.
+// they issue in 73% of the cycles and the matrix unit runs in 36%.  With parts
+// of a cached context (chunks, below) they issue in 53% and the matrix unit
+// runs in 34%: a sequence's tiles are cut into equal whole numbers of parts, so
+// the longest item has 80 key tiles where the mean has 63.
 //
 // Measured, D = 128, 32 query and 8 kv heads: a prompt of 8192 tokens, window
-// 4096, capped, MXFP4: 491 us (840 TFLOP/s of the products); 4 sequences with
-// up to 512 new tokens over 6144, NVFP4 4/6: 138 us with the join (722
-// TFLOP/s).  When they were measured side by side (522 and 158 us then), tiles
+// 4096, capped, MXFP4: 481 to 490 us (850 TFLOP/s of the products); 4 sequences
+// with up to 512 new tokens over 6144, NVFP4 4/6: 136 to 139 us with the join
+// (730 TFLOP/s).  When they were measured side by side (522 and 158 us then), tiles
 // of 64 keys and two waves a SIMD took the same on the prompt and 169 us on the
 // chunks.
 //
