@@ -35,12 +35,16 @@ STATUS = {0: "FP4_OK", -1: "FP4_E_NULL", -2: "FP4_E_SHAPE", -3: "FP4_E_ALIGN",
           -4: "FP4_E_FLAGS", -5: "FP4_E_WORKSPACE", -6: "FP4_E_HIP"}
 
 ROPE_INTERLEAVED = 1 << 0
+ROW_ALPHA = 1 << 8
 
 EXPORTS = ("fp4_workspace_bytes", "fp4_tensor_amax", "nvfp4_quantize", "nvfp4_quantize_noalloc",
            "nvfp4_quantize_rows",
            "nvfp4_requantize_t", "mxfp4_quantize", "mxfp4_gemm", "fp4_dequantize",
            "fp4_kv_write", "fp4_kv_read", "fp4_kv_attention_workspace_bytes", "fp4_kv_attention",
            "qk_norm_rope", "qk_norm_rope_workspace_bytes", "qk_norm_rope_backward",
+           "fp4_linear_workspace_bytes", "fp4_linear", "expert_route", "expert_route_backward",
+           "fp4_experts_workspace_bytes", "fp4_experts", "residual_norm",
+           "residual_norm_workspace_bytes", "residual_norm_backward",
            "fp4_status_str", "fp4_abi_version")
 
 
@@ -69,6 +73,29 @@ class _CRope(C.Structure):
                 ("table_rows", C.c_int64), ("q_heads", C.c_int32), ("k_heads", C.c_int32),
                 ("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("eps", C.c_float),
                 ("flags", C.c_uint32)]
+
+
+class _CWeights(C.Structure):
+    """fp4_weights of include/fp4q.h."""
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("alpha", C.c_void_p),
+                ("experts", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("format", C.c_int32), ("flags", C.c_uint32)]
+
+
+class _CRouting(C.Structure):
+    """fp4_routing of include/fp4q.h."""
+    _fields_ = [("logits", C.c_void_p), ("stride", C.c_int64), ("tokens", C.c_int64),
+                ("bias", C.c_void_p)] + [(n, C.c_int32) for n in (
+                    "experts", "top_k", "groups", "top_groups", "group_top", "sigmoid",
+                    "renormalize", "logits_bf16")] + [("scale", C.c_float)]
+
+
+class _CResidual(C.Structure):
+    """fp4_residual of include/fp4q.h."""
+    _fields_ = [("x", C.c_void_p), ("block", C.c_void_p), ("x_stride", C.c_int64),
+                ("block_stride", C.c_int64), ("tokens", C.c_int64), ("block_weight", C.c_void_p),
+                ("weight", C.c_void_p), ("gate", C.c_void_p), ("token_gate", C.c_int32),
+                ("dim", C.c_int32), ("scale", C.c_float), ("eps", C.c_float)]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4q.so")
@@ -126,6 +153,25 @@ def lib():
         L.qk_norm_rope_backward.restype = C.c_int
         L.qk_norm_rope_backward.argtypes = [rope, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp,
                                             sz, vp]
+        weights, routing, residual = (C.POINTER(t) for t in (_CWeights, _CRouting, _CResidual))
+        L.fp4_linear_workspace_bytes.restype = sz
+        L.fp4_linear_workspace_bytes.argtypes = [weights, i64]
+        L.fp4_linear.restype = C.c_int
+        L.fp4_linear.argtypes = [weights, vp, i64, i64, vp, i64, C.c_int, vp, sz, vp]
+        L.expert_route.restype = C.c_int
+        L.expert_route.argtypes = [routing, vp, vp, vp]
+        L.expert_route_backward.restype = C.c_int
+        L.expert_route_backward.argtypes = [routing, vp, vp, vp, i64, vp]
+        L.fp4_experts_workspace_bytes.restype = sz
+        L.fp4_experts_workspace_bytes.argtypes = [weights, weights, i64, i64]
+        L.fp4_experts.restype = C.c_int
+        L.fp4_experts.argtypes = [weights, weights, vp, i64, i64, vp, vp, i64, vp, i64, vp, sz, vp]
+        L.residual_norm.restype = C.c_int
+        L.residual_norm.argtypes = [residual, vp, i64, vp, i64, vp]
+        L.residual_norm_workspace_bytes.restype = sz
+        L.residual_norm_workspace_bytes.argtypes = [i64, C.c_int]
+        L.residual_norm_backward.restype = C.c_int
+        L.residual_norm_backward.argtypes = [residual] + [vp, i64] * 4 + [vp, vp, vp, vp, sz, vp]
         L.fp4_status_str.restype = C.c_char_p
         L.fp4_status_str.argtypes = [C.c_int]
         L.fp4_abi_version.restype = C.c_int
@@ -548,3 +594,209 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, t
     [head_dim] (None without a weight)."""
     return _binding().norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, table,
                                          eps, interleaved, out, ws, stream)
+
+
+# ------------------------------------------------------------------ FP4 weights
+class Fp4Weights:
+    """FP4 weights of a matrix, or of one for every expert: the buffers of
+    ``fp4_weights`` (include/fp4q.h), as ``nvfp4_quantize``,
+    ``nvfp4_quantize_rows`` or ``mxfp4_quantize`` (without HAD32) make them.
+
+    codes [rows][cols/2] or [experts][rows][cols/2]; scales [..][rows][cols/G]
+    or, NVFP4 of 16x16 tiles, [..][rows/16][cols/16]; NVFP4's alpha is one
+    float32 a matrix ([1] or [experts]) or one a row ([..][rows]).  The fields
+    are fixed, since the calls use the addresses taken here."""
+
+    __slots__ = ("codes", "scales", "alpha", "fmt", "flags", "experts", "rows", "cols", "_c", "_at")
+
+    def __init__(self, codes, scales, alpha=None, fmt=FORMAT_NVFP4):
+        torch = _torch()
+        if codes.dim() not in (2, 3):
+            raise ValueError("codes must be [rows][cols/2] or [experts][rows][cols/2], got %s" % (
+                tuple(codes.shape),))
+        lead, (rows, half) = tuple(codes.shape[:-2]), codes.shape[-2:]
+        cols, group = half * 2, 16 if fmt == FORMAT_NVFP4 else 32
+        _ints(codes, torch.uint8, lead + (rows, half), "codes")
+        flags = 0
+        if fmt == FORMAT_NVFP4:
+            by_tile = lead + (rows // 16, cols // 16)
+            if tuple(scales.shape) == by_tile != lead + (rows, cols // 16) and rows % 16 == 0:
+                flags |= BLOCK2D
+        _ints(scales, torch.uint8, by_tile if flags else lead + (rows, cols // group), "scales")
+        if fmt == FORMAT_NVFP4:
+            if alpha is None:
+                raise ValueError("NVFP4 needs alpha")
+            by_row = lead + (rows,)
+            one = lead or (1,)
+            if tuple(alpha.shape) == by_row != one:
+                flags |= ROW_ALPHA
+            _ints(alpha, torch.float32, by_row if flags & ROW_ALPHA else one, "alpha")
+        elif alpha is not None:
+            raise ValueError("MXFP4 has no alpha")
+        for t in (scales, alpha):
+            if t is not None and t.device != codes.device:
+                raise ValueError("the weights' tensors are on different devices: %s and %s" % (
+                    codes.device, t.device))
+        experts = lead[0] if lead else 1
+        c = _CWeights(codes.data_ptr(), scales.data_ptr(), _ptr(alpha), experts, rows, cols, fmt,
+                      flags)
+        for name, value in zip(self.__slots__, (codes, scales, alpha, fmt, flags, experts, rows, cols,
+                                                c, _Address(c, codes.device.index))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("the fields of a weights handle are fixed: %s" % name)
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def __copy__(self):
+        return self
+
+
+def fp4_linear(w, x, dtype=None, out=None, ws=None, stream=None):
+    """x [tokens][cols] (bf16) times the transpose of FP4 weights ``w``
+    [rows][cols]: [tokens][rows] in bf16, or float32 with ``dtype``.  The
+    products are exact and summed in fp32.  There is no backward: an x that
+    requires a gradient is refused in grad mode."""
+    torch = _torch()
+    if dtype not in (None, torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32, got %s" % (dtype,))
+    return _binding().linear(w._at, x, dtype is torch.float32, out, ws, stream)
+
+
+# ------------------------------------------------------------------ experts
+def expert_route(logits, top_k, scores="softmax", bias=None, groups=1, top_groups=1, group_top=1,
+                 renormalize=True, scale=1.0, out=None, stream=None):
+    """The ``top_k`` experts of each token from ``logits`` [tokens][experts]
+    (float32 or bf16): (weights [tokens][top_k] float32, experts int32).
+
+    With s the softmax or sigmoid of the logits, candidates are in the order of
+    the logits or, with ``bias`` [experts] (float32), of s + bias; of several
+    ``groups`` only the ``top_groups`` largest stay, by their largest candidate
+    or the sum of their two largest scores (``group_top`` 2).  Weights are
+    ``scale`` s, over the sum of the chosen s with ``renormalize``.  An expert
+    whose logit is -inf is never chosen; places left get expert -1 and weight
+    0.  Where logits require a gradient the weights carry it through torch's
+    autograd, by ``expert_route_backward``; ``out`` is refused then."""
+    return _binding().route(logits, top_k, scores, bias, groups, top_groups, group_top, renormalize,
+                            scale, out, stream)
+
+
+_expert_route_function = None
+
+
+def _expert_route_autograd(*args):
+    """expert_route(logits, top_k, scores, bias, groups, top_groups, group_top,
+    renormalize, scale, stream) as a node of torch's autograd graph."""
+    global _expert_route_function
+    if _expert_route_function is None:
+        torch = _torch()
+
+        class ExpertRoute(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, top_k, scores, bias, groups, top_groups, group_top, renormalize,
+                        scale, stream):
+                w, e = expert_route(logits, top_k, scores, bias, groups, top_groups, group_top,
+                                    renormalize, scale, stream=stream)
+                ctx.save_for_backward(logits, e)
+                ctx.how = scores, renormalize, scale
+                ctx.mark_non_differentiable(e)
+                return w, e
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dweights, _):
+                logits, e = ctx.saved_tensors
+                return (expert_route_backward(dweights.contiguous(), logits, e, *ctx.how),) + \
+                    (None,) * 9
+
+        _expert_route_function = ExpertRoute
+    return _expert_route_function.apply(*args)
+
+
+def expert_route_backward(dweights, logits, experts, scores="softmax", renormalize=True, scale=1.0,
+                          out=None, stream=None):
+    """The gradient of the logits (in their type) from that of
+    ``expert_route``'s weights and the experts that it chose."""
+    return _binding().route_backward(dweights, logits, experts, scores, renormalize, scale, out,
+                                     stream)
+
+
+def fp4_experts_workspace_bytes(gate_up, down, tokens, top_k):
+    """Bytes of workspace of ``fp4_experts`` for these weights and sizes."""
+    return _binding().experts_ws(gate_up._at, down._at, tokens, top_k)
+
+
+def fp4_experts(gate_up, down, x, weights, experts, out=None, ws=None, stream=None):
+    """The routed experts of each token, out[t] = sum_j weights[t][j]
+    D_e (silu(G_e x[t]) * (U_e x[t])) with e = experts[t][j].
+
+    ``gate_up`` holds the experts' G and U [experts][2F][cols] (the first F
+    rows are G's), ``down`` their D [experts][cols][F]; x [tokens][cols] bf16,
+    weights [tokens][top_k] float32, experts [tokens][top_k] int32 (numbers
+    outside the experts are skipped), as ``expert_route`` returns them.  There
+    is no backward: tensors that require a gradient are refused in grad mode."""
+    return _binding().experts(gate_up._at, down._at, x, weights, experts, out, ws, stream)
+
+
+# ------------------------------------------------------------------ norms around a block
+def residual_norm(x, block, weight, block_weight=None, gate=None, scale=1.0, eps=1e-6, out=None,
+                  stream=None):
+    """The end of one block and the start of the next: y = ``scale`` x + gate *
+    norm(block) and z = norm(y), as (y, z), all [tokens][dim] bf16.
+
+    norm(block) is block's RMS norm times ``block_weight`` [dim], or block
+    itself without it; norm(y) is y's times ``weight`` [dim].  ``gate`` is one
+    number for every channel ([dim]) or for every token ([tokens][1]), or None;
+    all bf16.  ``out`` may supply (y, z) and may be (x, block) themselves.
+    Where an input requires a gradient (and grad mode is on) the results carry
+    it through torch's autograd, by ``residual_norm_backward``; ``out`` is
+    refused then."""
+    return _binding().residual(x, block, weight, block_weight, gate, scale, eps, out, stream)
+
+
+_residual_norm_function = None
+
+
+def _flat_rows(g):
+    """g [tokens][dim] laid out as the calls take it."""
+    fits = (g.stride(1) == 1 and g.stride(0) >= g.shape[1] and g.stride(0) % 8 == 0 and
+            g.data_ptr() % 16 == 0)
+    return g if fits else g.clone(memory_format=_torch().contiguous_format)
+
+
+def _residual_norm_autograd(*args):
+    """residual_norm(x, block, weight, block_weight, gate, scale, eps, stream) as
+    a node of torch's autograd graph."""
+    global _residual_norm_function
+    if _residual_norm_function is None:
+        torch = _torch()
+
+        class ResidualNorm(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, block, weight, block_weight, gate, scale, eps, stream):
+                ctx.save_for_backward(x, block, weight, block_weight, gate)
+                ctx.how = scale, eps
+                return residual_norm(x, block, weight, block_weight, gate, scale, eps, stream=stream)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy, dz):
+                dx, db, dbw, dw, dg = residual_norm_backward(
+                    _flat_rows(dy), _flat_rows(dz), *ctx.saved_tensors, *ctx.how)
+                return tuple(None if g is None or not need else g.to(torch.bfloat16)
+                             for g, need in zip((dx, db, dw, dbw, dg), ctx.needs_input_grad)) + \
+                    (None,) * 3
+
+        _residual_norm_function = ResidualNorm
+    return _residual_norm_function.apply(*args)
+
+
+def residual_norm_backward(dy, dz, x, block, weight, block_weight=None, gate=None, scale=1.0,
+                           eps=1e-6, out=None, ws=None, stream=None):
+    """Gradients of ``residual_norm`` on the same arguments: (dx, dblock,
+    dblock_weight, dweight, dgate), dx and dblock bf16 (``out`` may supply
+    them), the others float32 (None without that input)."""
+    return _binding().residual_backward(dy, dz, x, block, weight, block_weight, gate, scale, eps, out,
+                                        ws, stream)

@@ -1,5 +1,5 @@
-// binding.cpp -- the Python calls of the FP4 cache, its attention and the norm
-// with rotation: checks of the tensors, allocation of outputs and workspace,
+// binding.cpp -- the Python calls of the FP4 cache, its attention, the norm with
+// rotation and the feed-forward operators (binding_feedforward.h): checks of the tensors, allocation of outputs and workspace,
 // and the call into libfp4q.so.  These calls are short (a decoding step's
 // kernels take microseconds), so their checks run here rather than in Python:
 // the norm of one decoding batch takes 5.5 us a call (17.3 through ctypes and torch.empty).
@@ -9,6 +9,7 @@
 // would be lost.
 #include <Python.h>
 
+#include <cstring>
 #include <string>
 
 #include <ATen/core/Tensor.h>
@@ -428,6 +429,8 @@ PyObject* norm_rope_backward(PyObject* const* a) {
   return r;
 }
 
+#include "binding_feedforward.h"
+
 // Calls take exactly N positional arguments; C++ exceptions end here.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -451,6 +454,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     FP4Q_ENTRY(kv_write, 5),      FP4Q_ENTRY(kv_read, 4),   FP4Q_ENTRY(kv_attention_ws, 9),
     FP4Q_ENTRY(kv_attention, 14), FP4Q_ENTRY(norm_rope, 10), FP4Q_ENTRY(norm_rope_backward, 13),
+    FP4Q_ENTRY(linear, 6),        FP4Q_ENTRY(experts, 8),   FP4Q_ENTRY(experts_ws, 4),
+    FP4Q_ENTRY(route, 11),        FP4Q_ENTRY(route_backward, 8), FP4Q_ENTRY(residual, 9),
+    FP4Q_ENTRY(residual_backward, 12),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,

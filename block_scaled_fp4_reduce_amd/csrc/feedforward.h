@@ -1,0 +1,446 @@
+// feedforward.h -- entry points of the feed-forward operators (products with
+// FP4 weights, routing, experts, the norms around a block), compiled as part of
+// fp4q.hip: argument checks on the host, then kernel launches on the caller's
+// stream.  See include/fp4q.h for the contract.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "experts_kernels.h"
+#include "host_common.h"
+#include "linear_kernels.h"
+#include "residual_kernels.h"
+#include "route_kernels.h"
+
+namespace fp4q {
+namespace feedforward {
+
+// ------------------------------------------------------------------ weights
+inline int check_weights(const fp4_weights* w) {
+  if (!w) return FP4_E_NULL;
+  if (w->format != FP4_FORMAT_NVFP4 && w->format != FP4_FORMAT_MXFP4) return FP4_E_FLAGS;
+  const bool nv = w->format == FP4_FORMAT_NVFP4;
+  if (w->flags & ~(uint32_t)(nv ? FP4_BLOCK2D | FP4_ROW_ALPHA : 0)) return FP4_E_FLAGS;
+  constexpr int64_t most = (int64_t)1 << 24;
+  if (w->experts < 0 || w->experts > most || w->rows < 0 || w->rows >= most || w->cols < 0 ||
+      w->cols >= most || w->cols % 32 || ((w->flags & FP4_BLOCK2D) && w->rows % 16))
+    return FP4_E_SHAPE;
+  if (w->rows > 0 && w->cols > 0 && w->experts > kMaxElems / (w->rows * w->cols)) return FP4_E_SHAPE;
+  if (w->experts * w->rows == 0) return FP4_OK;
+  if ((w->cols && (!w->codes || !w->scales)) || (nv && !w->alpha)) return FP4_E_NULL;
+  return aligned(w->codes, 16) && aligned(w->scales, 2) && aligned(w->alpha, 4) ? FP4_OK : FP4_E_ALIGN;
+}
+
+inline WeightView weight_view(const fp4_weights* w) {
+  const bool nv = w->format == FP4_FORMAT_NVFP4, tiles = w->flags & FP4_BLOCK2D;
+  const bool by_row = w->flags & FP4_ROW_ALPHA;
+  WeightView v;
+  v.codes = w->codes;
+  v.scales = w->scales;
+  v.alpha = nv ? w->alpha : nullptr;
+  v.codes_e = w->rows * (w->cols / 2);
+  v.scales_e = (tiles ? w->rows / 16 : w->rows) * (w->cols / (nv ? 16 : 32));
+  v.alpha_e = by_row ? w->rows : 1;
+  v.rows = (int)w->rows;
+  v.cols = (int)w->cols;
+  v.tile_shift = tiles ? 4 : 0;
+  v.row_alpha = by_row;
+  return v;
+}
+
+// Rows of `width` elements, `stride` apart.
+inline int check_rows(int64_t tokens, int64_t stride, int64_t width, int64_t multiple) {
+  if (stride < width || stride % multiple || stride >= kMaxElems) return FP4_E_SHAPE;
+  return tokens > 0 && stride > kMaxElems / tokens ? FP4_E_SHAPE : FP4_OK;
+}
+
+// ------------------------------------------------------------------ few tokens
+// Waves that share a row's K, the fewest that give every CU two workgroups (or
+// have a step of K each): fewer meet in fewer joins.
+inline void cut_rows(ColsArgs& a, int rows, int64_t slots, int r) {
+  const int steps = (a.w.cols + kColsStep - 1) / kColsStep;
+  a.wk = 1;
+  while (a.wk < kColsWaves && a.wk < steps &&
+         cdiv(rows, 16 * r * (kColsWaves / a.wk)) * slots < 2 * num_cus())
+    a.wk *= 2;
+  a.row_blocks = (int)cdiv(rows, 16 * r * (kColsWaves / a.wk));
+}
+
+template <int NT, int R, bool GATED, int SRC>
+hipError_t launch_cols(int format, const ColsArgs& a, int64_t slots, hipStream_t st) {
+  const unsigned grid = (unsigned)(slots * a.row_blocks);
+  return format == FP4_FORMAT_NVFP4
+             ? launch(fp4_cols_kernel<0, NT, R, GATED, SRC>, grid, kColsThreads, st, a)
+             : launch(fp4_cols_kernel<1, NT, R, GATED, SRC>, grid, kColsThreads, st, a);
+}
+
+inline int linear_tiles(int64_t tokens) { return tokens <= 16 ? 1 : (tokens <= 32 ? 2 : 4); }
+
+// ------------------------------------------------------------------ experts
+struct ExpertsPlan {
+  int64_t n;                             // assignments
+  bool inline_rows;                      // sorted by every workgroup for itself
+  size_t h, y, off, order, bytes;        // places in the workspace
+};
+
+inline ExpertsPlan experts_plan(const fp4_weights* gu, const fp4_weights* dn, int64_t tokens,
+                                int64_t top_k) {
+  ExpertsPlan p;
+  p.n = tokens * top_k;
+  p.inline_rows = p.n <= kInlineMost;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  p.h = take((size_t)p.n * dn->cols * 2);
+  p.y = take((size_t)p.n * dn->rows * 4);
+  p.off = take(p.inline_rows ? 0 : (size_t)(gu->experts + 1) * 4);
+  p.order = take(p.inline_rows ? 0 : (size_t)p.n * 4);
+  p.bytes = at;
+  return p;
+}
+
+inline int check_experts(const fp4_weights* gu, const fp4_weights* dn, int64_t tokens,
+                         int64_t top_k) {
+  if (int rc = check_weights(gu)) return rc;
+  if (int rc = check_weights(dn)) return rc;
+  if (gu->experts != dn->experts || gu->experts < 1 || gu->experts > 1024 ||
+      gu->rows != 2 * dn->cols || gu->cols != dn->rows || gu->cols == 0 || dn->cols == 0)
+    return FP4_E_SHAPE;
+  if (tokens < 0 || top_k < 1 || top_k > 1024 || tokens >= ((int64_t)1 << 27) ||
+      tokens * top_k >= ((int64_t)1 << 27))
+    return FP4_E_SHAPE;
+  return FP4_OK;
+}
+
+// ------------------------------------------------------------------ routing
+inline int check_route(const fp4_routing* r) {
+  if (!r) return FP4_E_NULL;
+  if (r->tokens < 0 || r->tokens >= ((int64_t)1 << 31) || r->experts < 1 || r->experts > 1024 ||
+      r->top_k < 1 || r->top_k > 64 || r->top_k > r->experts)
+    return FP4_E_SHAPE;
+  if (int rc = check_rows(r->tokens, r->stride, r->experts, 1)) return rc;
+  if (!std::isfinite(r->scale)) return FP4_E_SHAPE;
+  if (r->tokens > 0 && !r->logits) return FP4_E_NULL;
+  return aligned(r->logits, r->logits_bf16 ? 2 : 4) ? FP4_OK : FP4_E_ALIGN;
+}
+
+inline int check_choice(const fp4_routing* r) {
+  if (r->groups < 1 || r->groups > 64 || r->experts % r->groups || r->top_groups < 1 ||
+      r->top_groups > r->groups || r->group_top < 1 || r->group_top > 2 ||
+      r->experts / r->groups * r->top_groups < r->top_k)
+    return FP4_E_SHAPE;
+  return aligned(r->bias, 4) ? FP4_OK : FP4_E_ALIGN;
+}
+
+inline RouteArgs route_args(const fp4_routing* r) {
+  RouteArgs a;
+  a.logits = r->logits;
+  a.bias = r->bias;
+  a.stride = r->stride;
+  a.tokens = r->tokens;
+  a.experts = r->experts;
+  a.top_k = r->top_k;
+  a.groups = r->top_groups < r->groups ? r->groups : 1;      // all groups stay: none to choose
+  a.top_groups = r->top_groups;
+  a.group_top = r->group_top;
+  a.renormalize = r->renormalize;
+  a.scale = r->scale;
+  return a;
+}
+
+// f(values a lane) with that as a compile-time constant.
+template <typename F>
+hipError_t route_variant(int experts, F&& f) {
+  if (experts <= 64) return f(std::integral_constant<int, 1>{});
+  if (experts <= 128) return f(std::integral_constant<int, 2>{});
+  if (experts <= 256) return f(std::integral_constant<int, 4>{});
+  if (experts <= 512) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
+
+// ------------------------------------------------------------------ norms around a block
+inline int check_residual(const fp4_residual* a) {
+  if (!a) return FP4_E_NULL;
+  if (a->tokens < 0 || a->tokens >= ((int64_t)1 << 31) || a->dim < 8 || a->dim > 16384 ||
+      a->dim % 8)
+    return FP4_E_SHAPE;
+  if (!(a->eps >= 0.0f) || std::isinf(a->eps) || !std::isfinite(a->scale)) return FP4_E_SHAPE;
+  if (!a->weight) return FP4_E_NULL;
+  if (!aligned(a->weight, 16) || !aligned(a->block_weight, 16) ||
+      !aligned(a->gate, a->token_gate ? 2 : 16))
+    return FP4_E_ALIGN;
+  return FP4_OK;
+}
+
+inline int check_residual_pair(const fp4_residual* a, const void* p, int64_t ps, const void* q,
+                               int64_t qs) {
+  if (a->tokens == 0) return FP4_OK;
+  if (!p || !q) return FP4_E_NULL;
+  if (int rc = check_rows(a->tokens, ps, a->dim, 8)) return rc;
+  if (int rc = check_rows(a->tokens, qs, a->dim, 8)) return rc;
+  return aligned(p, 16) && aligned(q, 16) ? FP4_OK : FP4_E_ALIGN;
+}
+
+inline ResidualArgs residual_args(const fp4_residual* a) {
+  ResidualArgs r;
+  r.x = a->x;
+  r.b = a->block;
+  r.bw = a->block_weight;
+  r.w = a->weight;
+  r.gate = a->gate;
+  r.xs = a->x_stride;
+  r.bs = a->block_stride;
+  r.tokens = a->tokens;
+  r.dim = a->dim;
+  r.token_gate = a->token_gate != 0;
+  r.scale = a->scale;
+  r.eps = a->eps;
+  return r;
+}
+
+// f(waves a row, chunks a thread).
+template <typename F>
+hipError_t residual_variant(int dim, F&& f) {
+  using std::integral_constant;
+  if (dim <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if (dim <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  if (dim <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (dim <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (dim <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+}
+
+inline int64_t residual_groups(int64_t tokens, int dim) {
+  const int64_t g = dim <= 1024 ? cdiv(tokens, RowShape<1>::kRows) : tokens;
+  return g < kResidualMaxGroups ? g : kResidualMaxGroups;
+}
+
+}  // namespace feedforward
+}  // namespace fp4q
+
+extern "C" {
+
+size_t fp4_linear_workspace_bytes(const fp4_weights*, int64_t) { return 0; }
+
+int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_t tokens, void* out,
+               int64_t out_stride, int out_f32, void* ws, size_t ws_bytes, void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_weights(w)) return rc;
+  if (w->experts != 1 || tokens < 0 || tokens >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
+  if (tokens == 0 || w->rows == 0) return FP4_OK;
+  if ((!x && w->cols) || !out) return FP4_E_NULL;
+  if (int rc = check_rows(tokens, x_stride, w->cols, 8)) return rc;
+  if (int rc = check_rows(tokens, out_stride, w->rows, 1)) return rc;
+  if (!aligned(x, 16) || !aligned(out, out_f32 ? 4 : 2)) return FP4_E_ALIGN;
+  ColsArgs a = {};
+  a.w = weight_view(w);
+  a.x = x;
+  a.out = out;
+  a.xs = x_stride;
+  a.os = out_stride;
+  a.tokens = tokens;
+  a.out_f32 = out_f32 != 0;
+  a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
+  const int nt = linear_tiles(tokens);
+  const int64_t slots = cdiv(tokens, 16 * nt);
+  cut_rows(a, a.w.rows, slots, 1);
+  if (slots * a.row_blocks >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
+  hipStream_t st = (hipStream_t)stream;
+  switch (nt) {
+    case 1: return launched(launch_cols<1, 1, false, kDense>(w->format, a, slots, st));
+    case 2: return launched(launch_cols<2, 1, false, kDense>(w->format, a, slots, st));
+    default: return launched(launch_cols<4, 1, false, kDense>(w->format, a, slots, st));
+  }
+}
+
+int expert_route(const fp4_routing* r, float* weights, int32_t* experts, void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_route(r)) return rc;
+  if (int rc = check_choice(r)) return rc;
+  if (r->tokens == 0) return FP4_OK;
+  if (!weights || !experts) return FP4_E_NULL;
+  if (!aligned(weights, 4) || !aligned(experts, 4)) return FP4_E_ALIGN;
+  const RouteArgs a = route_args(r);
+  const unsigned grid = (unsigned)cdiv(a.tokens, kRouteWaves);
+  const bool wide = a.bias || (a.groups > 1 && a.group_top == 2);
+  return launched(route_variant(a.experts, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    auto go = [&](auto kernel) {
+      return launch(kernel, grid, kRouteThreads, (hipStream_t)stream, a, (int)(r->sigmoid != 0),
+                    weights, experts);
+    };
+    if (wide)
+      return r->logits_bf16 ? go(expert_route_kernel<double, V, true>)
+                            : go(expert_route_kernel<double, V, false>);
+    return r->logits_bf16 ? go(expert_route_kernel<float, V, true>)
+                          : go(expert_route_kernel<float, V, false>);
+  }));
+}
+
+int expert_route_backward(const fp4_routing* r, const float* dweights, const int32_t* experts,
+                          void* dlogits, int64_t dlogits_stride, void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_route(r)) return rc;
+  if (int rc = check_rows(r->tokens, dlogits_stride, r->experts, 1)) return rc;
+  if (r->tokens == 0) return FP4_OK;
+  if (!dweights || !experts || !dlogits) return FP4_E_NULL;
+  if (!aligned(dweights, 4) || !aligned(experts, 4) || !aligned(dlogits, r->logits_bf16 ? 2 : 4))
+    return FP4_E_ALIGN;
+  RouteArgs a = route_args(r);
+  a.bias = nullptr;
+  const unsigned grid = (unsigned)cdiv(a.tokens, kRouteWaves);
+  return launched(route_variant(a.experts, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    auto go = [&](auto kernel) {
+      return launch(kernel, grid, kRouteThreads, (hipStream_t)stream, a, (int)(r->sigmoid != 0),
+                    dweights, experts, dlogits, dlogits_stride);
+    };
+    return r->logits_bf16 ? go(expert_route_backward_kernel<V, true>)
+                          : go(expert_route_backward_kernel<V, false>);
+  }));
+}
+
+size_t fp4_experts_workspace_bytes(const fp4_weights* gate_up, const fp4_weights* down,
+                                   int64_t tokens, int64_t top_k) {
+  using namespace fp4q::feedforward;
+  if (check_experts(gate_up, down, tokens, top_k) || tokens == 0) return 0;
+  return experts_plan(gate_up, down, tokens, top_k).bytes;
+}
+
+int fp4_experts(const fp4_weights* gate_up, const fp4_weights* down, const uint16_t* x,
+                int64_t x_stride, int64_t tokens, const float* weights, const int32_t* experts,
+                int64_t top_k, uint16_t* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_experts(gate_up, down, tokens, top_k)) return rc;
+  if (tokens == 0) return FP4_OK;
+  if (!x || !weights || !experts || !out || !ws) return FP4_E_NULL;
+  if (int rc = check_rows(tokens, x_stride, gate_up->cols, 8)) return rc;
+  if (int rc = check_rows(tokens, out_stride, gate_up->cols, 8)) return rc;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(weights, 4) || !aligned(experts, 4) ||
+      !aligned(ws, 16))
+    return FP4_E_ALIGN;
+  const ExpertsPlan p = experts_plan(gate_up, down, tokens, top_k);
+  if (ws_bytes < p.bytes) return FP4_E_WORKSPACE;
+  uint8_t* const base = (uint8_t*)ws;
+  hipStream_t st = (hipStream_t)stream;
+  const int e = (int)gate_up->experts, inner = (int)down->cols;
+  ColsArgs a = {};
+  a.w = weight_view(gate_up);
+  a.x = x;
+  a.out = base + p.h;
+  a.xs = x_stride;
+  a.os = inner;
+  a.tokens = tokens;
+  a.ids = experts;
+  a.off = (const int32_t*)(base + p.off);
+  a.order = (const int32_t*)(base + p.order);
+  a.top_k = (int)top_k;
+  a.experts = e;
+  a.inner = inner;
+  a.out_vec = 1;
+  a.x_per_token = 1;
+  ColsArgs b = a;
+  b.w = weight_view(down);
+  b.x = (const uint16_t*)(base + p.h);
+  b.out = base + p.y;
+  b.xs = inner;
+  b.os = down->rows;
+  b.out_f32 = 1;
+  b.x_per_token = 0;
+  const int64_t slots = p.inline_rows && p.n < e ? p.n : e;
+  cut_rows(a, inner, slots, 1);
+  cut_rows(b, b.w.rows, slots, 1);
+  if (slots * a.row_blocks >= ((int64_t)1 << 31) || slots * b.row_blocks >= ((int64_t)1 << 31))
+    return FP4_E_SHAPE;
+  hipError_t err = hipSuccess;
+  if (!p.inline_rows)
+    err = launch(expert_plan_kernel, (unsigned)e, kPlanThreads, st, experts, (int)p.n, e,
+                 (int32_t*)(base + p.off), (int32_t*)(base + p.order));
+  auto both = [&](auto nt, auto src) {
+    constexpr int N = decltype(nt)::value, S = decltype(src)::value;
+    err = first(err, launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
+    err = first(err, launch_cols<N, 1, false, S>(down->format, b, slots, st));
+  };
+  auto with = [&](auto src) {
+    if (p.n <= 16 * (int64_t)e) both(std::integral_constant<int, 1>{}, src);
+    else both(std::integral_constant<int, 4>{}, src);
+  };
+  if (p.inline_rows) with(std::integral_constant<int, kInline>{});
+  else with(std::integral_constant<int, kPlanned>{});
+  const int64_t quads = tokens * (down->rows / 4);
+  if (cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
+  err = first(err, launch(experts_join_kernel, (unsigned)cdiv(quads, kJoinThreads), kJoinThreads, st,
+                          (const float*)(base + p.y), weights, experts, tokens, (int)top_k, e,
+                          (int)down->rows, out, out_stride));
+  return launched(err);
+}
+
+int residual_norm(const fp4_residual* a, uint16_t* y, int64_t y_stride, uint16_t* z,
+                  int64_t z_stride, void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_residual(a)) return rc;
+  if (int rc = check_residual_pair(a, a->x, a->x_stride, a->block, a->block_stride)) return rc;
+  if (int rc = check_residual_pair(a, y, y_stride, z, z_stride)) return rc;
+  if (a->tokens == 0) return FP4_OK;
+  const ResidualArgs r = residual_args(a);
+  return launched(residual_variant(a->dim, [&](auto wpr, auto ch) {
+    constexpr int W = decltype(wpr)::value, CH = decltype(ch)::value;
+    return launch(residual_norm_kernel<W, CH>, (unsigned)cdiv(r.tokens, RowShape<W>::kRows),
+                  RowShape<W>::kAll, (hipStream_t)stream, r, y, y_stride, z, z_stride);
+  }));
+}
+
+size_t residual_norm_workspace_bytes(int64_t tokens, int dim) {
+  if (tokens < 0 || dim < 8 || dim > 16384) return 0;
+  return (size_t)fp4q::feedforward::residual_groups(tokens, dim) * 2 * (size_t)dim * sizeof(float);
+}
+
+int residual_norm_backward(const fp4_residual* a, const uint16_t* dy, int64_t dy_stride,
+                           const uint16_t* dz, int64_t dz_stride, uint16_t* dx, int64_t dx_stride,
+                           uint16_t* dblock, int64_t dblock_stride, float* dblock_weight,
+                           float* dweight, float* dgate, void* ws, size_t ws_bytes, void* stream) {
+  using namespace fp4q;
+  using namespace fp4q::feedforward;
+  if (int rc = check_residual(a)) return rc;
+  if (int rc = check_residual_pair(a, a->x, a->x_stride, a->block, a->block_stride)) return rc;
+  if (int rc = check_residual_pair(a, dy, dy_stride, dz, dz_stride)) return rc;
+  if (int rc = check_residual_pair(a, dx, dx_stride, dblock, dblock_stride)) return rc;
+  if ((dblock_weight && !a->block_weight) || (dgate && !a->gate)) return FP4_E_NULL;
+  const ResidualArgs r = residual_args(a);
+  const bool channel = a->gate && !a->token_gate;
+  const bool sums = dblock_weight || dweight || (dgate && channel);
+  if (!aligned(dblock_weight, 4) || !aligned(dweight, 4) || !aligned(dgate, 4) || !aligned(ws, 16))
+    return FP4_E_ALIGN;
+  const size_t need = residual_norm_workspace_bytes(a->tokens, a->dim);
+  if (sums && need > 0 && !ws) return FP4_E_NULL;
+  if (sums && ws_bytes < need) return FP4_E_WORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  const int64_t groups = residual_groups(a->tokens, a->dim);
+  hipError_t e = hipSuccess;
+  if (groups > 0)
+    e = residual_variant(a->dim, [&](auto wpr, auto ch) {
+      constexpr int W = decltype(wpr)::value, CH = decltype(ch)::value;
+      return launch(residual_norm_bwd_kernel<W, CH>, (unsigned)groups, RowShape<W>::kAll, st, r, dy,
+                    dy_stride, dz, dz_stride, dx, dx_stride, dblock, dblock_stride,
+                    sums ? (float*)ws : nullptr, dgate);
+    });
+  if (sums)
+    e = first(e, launch(residual_norm_dw_kernel, (unsigned)cdiv(2 * (int64_t)a->dim, kResidualDwCols),
+                        kResidualDwCols * kResidualDwRows, st, (const float*)ws, (int)groups, r,
+                        dblock_weight, dweight, dgate));
+  return launched(e);
+}
+
+}  // extern "C"

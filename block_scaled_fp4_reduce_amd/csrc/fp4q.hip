@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "../../include/fp4q.h"
+#include "feedforward.h"
 #include "host_common.h"
 #include "kv_cache_kernels.h"
 #include "kv_host.h"

@@ -396,6 +396,139 @@ int qk_norm_rope_backward(const fp4_qk_rope* x, const uint16_t* dq_out, int64_t 
                           int64_t dq_stride, uint16_t* dk, int64_t dk_stride, float* dq_weight,
                           float* dk_weight, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The feed-forward half of a layer: products with FP4 weights, routing to
+ * experts, the routed experts, and the norms around a block.
+ *
+ * Activations are bf16 [tokens][cols]; `*_stride` is the number of elements
+ * from one row to the next, at least the row's length and (but for the
+ * outputs of fp4_linear) a multiple of 8.  Pointers are 16-byte aligned where
+ * nothing else is said.  The structs are read by the call itself and need not
+ * outlive it.
+ * ------------------------------------------------------------------------ */
+
+enum { FP4_ROW_ALPHA = 1u << 8 };   /* fp4_weights: an alpha for every row */
+
+/* FP4 weights, one matrix [rows][cols] or one for each expert, as
+ * nvfp4_quantize (FP4_RTN6, FP4_FOUR_OVER_SIX, also FP4_BLOCK2D),
+ * nvfp4_quantize_rows or mxfp4_quantize (FP4_ROWWISE, no FP4_HAD32) lay them
+ * out, G = 16 (NVFP4) or 32 (MXFP4):
+ *   codes  [experts][rows][cols/2]
+ *   scales [experts][rows][cols/G], with FP4_BLOCK2D [experts][rows/16][cols/16]
+ *   alpha  NVFP4 only (else NULL): [experts], with FP4_ROW_ALPHA [experts][rows]
+ * A weight is q * Delta * alpha, or q * 2^(code-127).  The sign bit of an E4M3
+ * scale is ignored; the E4M3 code 0x7F and UE8M0 codes above 252 are outside
+ * the domain, and MXFP4 weights below 2^-126 may count as 0. */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;       /* 2-byte aligned                              */
+  const float* alpha;          /* 4-byte aligned                              */
+  int64_t experts;             /* 1 for a plain matrix                        */
+  int64_t rows, cols;          /* below 2^24; cols a multiple of 32, rows of 16
+                                  with FP4_BLOCK2D; experts x rows x cols at
+                                  most 2^40                                   */
+  int32_t format;              /* FP4_FORMAT_NVFP4 or FP4_FORMAT_MXFP4        */
+  uint32_t flags;              /* NVFP4: FP4_BLOCK2D, FP4_ROW_ALPHA; MXFP4: 0 */
+} fp4_weights;
+
+/* Device workspace of fp4_linear (no initialisation; may be 0). */
+size_t fp4_linear_workspace_bytes(const fp4_weights* w, int64_t tokens);
+
+/* out[t][n] = sum_k x[t][k] w[n][k] for one matrix (experts 1).  The products
+ * of x with q * Delta (or q * 2^k) are exact, their sums fp32, and alpha is
+ * applied to the sum.  out is bf16, or fp32 with out_f32, aligned to its
+ * elements, out_stride any number from rows on.  Equal calls give equal bits. */
+int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_t tokens,
+               void* out, int64_t out_stride, int out_f32, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts of each token.  With logits l [tokens][experts] and s = softmax(l)
+ * or sigmoid(l) over a token's experts, the candidates' order is by
+ *   c = l, or with a bias  c = s + bias  (computed in 64 bits).
+ * Experts whose logit or c is -inf or NaN are no candidates.  With groups G > 1
+ * (experts / G consecutive experts each) only the candidates of the top_groups
+ * groups of largest size stay; a group's size is its largest c, or with
+ * group_top 2 the sum of its two largest s (+ bias) among candidates.  The top_k
+ * candidates of largest c follow in that order (ties, of groups also: the lower
+ * index first), each with
+ *   weight = scale s_i, or with renormalize  scale s_i / sum of the chosen s.
+ * Places without a candidate get expert -1 and weight 0.  A NaN or +inf among
+ * softmax's logits makes the weights of its token NaN. */
+typedef struct {
+  const void* logits;          /* fp32 or bf16, aligned to its elements       */
+  int64_t stride;              /* elements between tokens, at least experts   */
+  int64_t tokens;
+  const float* bias;           /* [experts] or NULL                           */
+  int32_t experts, top_k;      /* 1 to 1024; 1 to 64 and at most experts      */
+  int32_t groups, top_groups;  /* groups divide the experts; top_groups of
+                                  them hold top_k experts at least            */
+  int32_t group_top;           /* 1 or 2                                      */
+  int32_t sigmoid;             /* 0: softmax                                  */
+  int32_t renormalize;
+  int32_t logits_bf16;
+  float scale;
+} fp4_routing;
+
+/* weights [tokens][top_k] fp32, experts [tokens][top_k]. */
+int expert_route(const fp4_routing* r, float* weights, int32_t* experts, void* stream);
+
+/* Gradient of the logits, in their type: from dweights [tokens][top_k] and the
+ * experts that the forward chose (numbers outside [0, experts) count as no
+ * expert).  The choice and the bias have no gradient: bias, groups, top_groups
+ * and group_top are not looked at. */
+int expert_route_backward(const fp4_routing* r, const float* dweights, const int32_t* experts,
+                          void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* Device workspace of fp4_experts (no initialisation). */
+size_t fp4_experts_workspace_bytes(const fp4_weights* gate_up, const fp4_weights* down,
+                                   int64_t tokens, int64_t top_k);
+
+/* out[t] = sum_j weights[t][j] D_e (silu(G_e x[t]) * (U_e x[t])), e =
+ * experts[t][j]: gate_up holds G_e (rows 0 .. F - 1) and U_e (rows F .. 2F - 1)
+ * [experts][2F][cols], down D_e [experts][cols][F].  The hidden values are
+ * rounded to bf16 between the products, sums and the rest are fp32.  Numbers
+ * outside [0, experts) are skipped; a token without an expert gets 0; an expert
+ * named twice counts twice.  tokens x top_k below 2^31 / 16, experts up to
+ * 1024.  out may not overlap x.  Equal calls give equal bits. */
+int fp4_experts(const fp4_weights* gate_up, const fp4_weights* down, const uint16_t* x,
+                int64_t x_stride, int64_t tokens, const float* weights, const int32_t* experts,
+                int64_t top_k, uint16_t* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                void* stream);
+
+/* The end of one block and the start of the next:
+ *   n = block / sqrt(mean(block^2) + eps) * block_weight  (or block without it)
+ *   y = scale x + gate n,   z = y / sqrt(mean(y^2) + eps) * weight
+ * with a gate for every channel, one for every token, or none (1). */
+typedef struct {
+  const uint16_t* x;           /* [tokens][dim] bf16: the residual stream     */
+  const uint16_t* block;       /* [tokens][dim] bf16: the block's output      */
+  int64_t x_stride, block_stride;
+  int64_t tokens;
+  const uint16_t* block_weight;/* [dim] bf16 or NULL: no norm of the block    */
+  const uint16_t* weight;      /* [dim] bf16                                  */
+  const uint16_t* gate;        /* bf16 [dim] or, with token_gate, [tokens]
+                                  (2-byte aligned); NULL: none                */
+  int32_t token_gate;
+  int32_t dim;                 /* a multiple of 8, 8 to 16384                 */
+  float scale, eps;
+} fp4_residual;
+
+/* Forward: y and z bf16 [tokens][dim].  y may be x and z may be block (with the
+ * same strides). */
+int residual_norm(const fp4_residual* a, uint16_t* y, int64_t y_stride, uint16_t* z,
+                  int64_t z_stride, void* stream);
+
+/* Device workspace of residual_norm_backward (no initialisation). */
+size_t residual_norm_workspace_bytes(int64_t tokens, int dim);
+
+/* Backward: from the gradients of y and z and the forward's inputs, those of x
+ * and block (bf16), and where wanted (else NULL) of block_weight, weight (fp32
+ * [dim]) and gate (fp32, shaped as gate), summed in an order that depends on
+ * the sizes alone.  dx may be dy and dblock may be dz. */
+int residual_norm_backward(const fp4_residual* a, const uint16_t* dy, int64_t dy_stride,
+                           const uint16_t* dz, int64_t dz_stride, uint16_t* dx, int64_t dx_stride,
+                           uint16_t* dblock, int64_t dblock_stride, float* dblock_weight,
+                           float* dweight, float* dgate, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* fp4_status_str(int status);
 
