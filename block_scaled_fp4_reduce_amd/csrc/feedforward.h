@@ -12,6 +12,7 @@
 #include "experts_kernels.h"
 #include "host_common.h"
 #include "linear_kernels.h"
+#include "linear_tiled_kernels.h"
 #include "residual_kernels.h"
 #include "route_kernels.h"
 
@@ -26,7 +27,7 @@ inline int check_weights(const fp4_weights* w) {
   if (w->flags & ~(uint32_t)(nv ? FP4_BLOCK2D | FP4_ROW_ALPHA : 0)) return FP4_E_FLAGS;
   constexpr int64_t most = (int64_t)1 << 24;
   if (w->experts < 0 || w->experts > most || w->rows < 0 || w->rows >= most || w->cols < 0 ||
-      w->cols >= most || w->cols % 32 || ((w->flags & FP4_BLOCK2D) && w->rows % 16))
+      w->cols >= most / 4 || w->cols % 32 || ((w->flags & FP4_BLOCK2D) && w->rows % 16))
     return FP4_E_SHAPE;
   if (w->rows > 0 && w->cols > 0 && w->experts > kMaxElems / (w->rows * w->cols)) return FP4_E_SHAPE;
   if (w->experts * w->rows == 0) return FP4_OK;
@@ -77,11 +78,47 @@ hipError_t launch_cols(int format, const ColsArgs& a, int64_t slots, hipStream_t
              : launch(fp4_cols_kernel<1, NT, R, GATED, SRC>, grid, kColsThreads, st, a);
 }
 
+// ------------------------------------------------------------------ many tokens
+template <bool GATED, bool EXPERTS>
+hipError_t launch_tiled(int format, TiledArgs a, hipStream_t st) {
+  a.tiles_n = (uint32_t)cdiv(GATED ? a.inner : a.w.rows, GATED ? kTileWeights / 2 : kTileWeights);
+  const int64_t grid = EXPERTS ? cdiv(a.tiles_t, 4 * kXcds) * 4 * kXcds * a.tiles_n
+                               : xcd_grid(a.tiles_t, a.tiles_n, 8, 8);
+  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  return format == FP4_FORMAT_NVFP4
+             ? launch(fp4_tiled_kernel<0, GATED, EXPERTS>, (unsigned)grid, kTiledThreads, st, a)
+             : launch(fp4_tiled_kernel<1, GATED, EXPERTS>, (unsigned)grid, kTiledThreads, st, a);
+}
+
+// What the two forms of a call have in common.
+inline TiledArgs tiled_args(const ColsArgs& a) {
+  TiledArgs t = {};
+  t.w = a.w;
+  t.x = a.x;
+  t.out = a.out;
+  t.xs = a.xs;
+  t.os = a.os;
+  t.tokens = a.tokens;
+  t.off = a.off;
+  t.order = a.order;
+  t.top_k = a.top_k;
+  t.experts = a.experts;
+  t.inner = a.inner;
+  t.x_per_token = a.x_per_token;
+  t.out_f32 = a.out_f32;
+  return t;
+}
+
 inline int linear_tiles(int64_t tokens) { return tokens <= 16 ? 1 : (tokens <= 32 ? 2 : 4); }
 
 // ------------------------------------------------------------------ experts
+// The tiled kernel addresses its rows of x and h in 31 bits: batches past that
+// go in slices of tokens, one after another in the same workspace.
+constexpr int64_t kSliceBytes = 0x7FFF0000;
+
 struct ExpertsPlan {
-  int64_t n;                             // assignments
+  int64_t tokens;                        // of a slice
+  int64_t n;                             // its assignments
   bool inline_rows;                      // sorted by every workgroup for itself
   size_t h, y, off, order, bytes;        // places in the workspace
 };
@@ -89,7 +126,9 @@ struct ExpertsPlan {
 inline ExpertsPlan experts_plan(const fp4_weights* gu, const fp4_weights* dn, int64_t tokens,
                                 int64_t top_k) {
   ExpertsPlan p;
-  p.n = tokens * top_k;
+  const int64_t most = kSliceBytes / (2 * top_k * dn->cols);
+  p.tokens = tokens < most ? tokens : most;
+  p.n = p.tokens * top_k;
   p.inline_rows = p.n <= kInlineMost;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -112,10 +151,76 @@ inline int check_experts(const fp4_weights* gu, const fp4_weights* dn, int64_t t
   if (gu->experts != dn->experts || gu->experts < 1 || gu->experts > 1024 ||
       gu->rows != 2 * dn->cols || gu->cols != dn->rows || gu->cols == 0 || dn->cols == 0)
     return FP4_E_SHAPE;
-  if (tokens < 0 || top_k < 1 || top_k > 1024 || tokens >= ((int64_t)1 << 27) ||
-      tokens * top_k >= ((int64_t)1 << 27))
-    return FP4_E_SHAPE;
+  if (tokens < 0 || tokens >= ((int64_t)1 << 31) || top_k < 1 || top_k > 64) return FP4_E_SHAPE;
   return FP4_OK;
+}
+
+inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* down,
+                                const ExpertsPlan& p, const uint16_t* x, int64_t x_stride,
+                                int64_t tokens, const float* weights, const int32_t* experts,
+                                int top_k, uint16_t* out, int64_t out_stride, uint8_t* ws,
+                                hipStream_t st) {
+  const int e = (int)gate_up->experts, inner = (int)down->cols;
+  const int64_t n = tokens * top_k;
+  ColsArgs a = {};
+  a.w = weight_view(gate_up);
+  a.x = x;
+  a.out = ws + p.h;
+  a.xs = x_stride;
+  a.os = inner;
+  a.tokens = tokens;
+  a.ids = experts;
+  a.off = (const int32_t*)(ws + p.off);
+  a.order = (const int32_t*)(ws + p.order);
+  a.top_k = top_k;
+  a.experts = e;
+  a.inner = inner;
+  a.out_vec = 1;
+  a.x_per_token = 1;
+  ColsArgs b = a;
+  b.w = weight_view(down);
+  b.x = (const uint16_t*)(ws + p.h);
+  b.out = ws + p.y;
+  b.xs = inner;
+  b.os = down->rows;
+  b.out_f32 = 1;
+  b.x_per_token = 0;
+  const int64_t slots = p.inline_rows && n < e ? n : e;
+  cut_rows(a, inner, slots, 1);
+  cut_rows(b, b.w.rows, slots, 1);
+  const int64_t quads = tokens * (down->rows / 4);
+  if (slots * a.row_blocks >= ((int64_t)1 << 31) || slots * b.row_blocks >= ((int64_t)1 << 31) ||
+      cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31))
+    return hipErrorInvalidConfiguration;
+  hipError_t err = hipSuccess;
+  if (!p.inline_rows)
+    err = launch(expert_plan_kernel, (unsigned)e, kPlanThreads, st, experts, (int)n, e,
+                 (int32_t*)(ws + p.off), (int32_t*)(ws + p.order));
+  auto both = [&](auto nt, auto src) {
+    constexpr int N = decltype(nt)::value, S = decltype(src)::value;
+    err = first(err, launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
+    err = first(err, launch_cols<N, 1, false, S>(down->format, b, slots, st));
+  };
+  auto with = [&](auto src) {
+    if (n <= 16 * (int64_t)e) both(std::integral_constant<int, 1>{}, src);
+    else both(std::integral_constant<int, 4>{}, src);
+  };
+  if (!p.inline_rows && n > 32 * (int64_t)e) {
+    TiledArgs ta = tiled_args(a), tb = tiled_args(b);
+    ta.tiles_t = tb.tiles_t = (uint32_t)(n / kTileTokens + e);
+    ta.out_vec = tb.out_vec = 1;
+    ta.x_bytes = ((tokens - 1) * x_stride + gate_up->cols) * 2;
+    tb.x_bytes = n * inner * 2;
+    err = first(err, launch_tiled<true, true>(gate_up->format, ta, st));
+    err = first(err, launch_tiled<false, true>(down->format, tb, st));
+  } else if (p.inline_rows) {
+    with(std::integral_constant<int, kInline>{});
+  } else {
+    with(std::integral_constant<int, kPlanned>{});
+  }
+  return first(err, launch(experts_join_kernel, (unsigned)cdiv(quads, kJoinThreads), kJoinThreads, st,
+                           (const float*)(ws + p.y), weights, experts, tokens, top_k, e,
+                           (int)down->rows, out, out_stride));
 }
 
 // ------------------------------------------------------------------ routing
@@ -248,6 +353,13 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
   a.tokens = tokens;
   a.out_f32 = out_f32 != 0;
   a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
+  if (tokens > 128 && cdiv(tokens, kTileTokens) * cdiv(w->rows, kTileWeights) >= 64 && w->cols > 0 &&
+      (kTileTokens * x_stride + w->cols) * 2 <= kSliceBytes) {
+    TiledArgs t = tiled_args(a);
+    t.tiles_t = (uint32_t)cdiv(tokens, kTileTokens);
+    t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
+    return launched(launch_tiled<false, false>(w->format, t, (hipStream_t)stream));
+  }
   const int nt = linear_tiles(tokens);
   const int64_t slots = cdiv(tokens, 16 * nt);
   cut_rows(a, a.w.rows, slots, 1);
@@ -332,57 +444,15 @@ int fp4_experts(const fp4_weights* gate_up, const fp4_weights* down, const uint1
     return FP4_E_ALIGN;
   const ExpertsPlan p = experts_plan(gate_up, down, tokens, top_k);
   if (ws_bytes < p.bytes) return FP4_E_WORKSPACE;
-  uint8_t* const base = (uint8_t*)ws;
-  hipStream_t st = (hipStream_t)stream;
-  const int e = (int)gate_up->experts, inner = (int)down->cols;
-  ColsArgs a = {};
-  a.w = weight_view(gate_up);
-  a.x = x;
-  a.out = base + p.h;
-  a.xs = x_stride;
-  a.os = inner;
-  a.tokens = tokens;
-  a.ids = experts;
-  a.off = (const int32_t*)(base + p.off);
-  a.order = (const int32_t*)(base + p.order);
-  a.top_k = (int)top_k;
-  a.experts = e;
-  a.inner = inner;
-  a.out_vec = 1;
-  a.x_per_token = 1;
-  ColsArgs b = a;
-  b.w = weight_view(down);
-  b.x = (const uint16_t*)(base + p.h);
-  b.out = base + p.y;
-  b.xs = inner;
-  b.os = down->rows;
-  b.out_f32 = 1;
-  b.x_per_token = 0;
-  const int64_t slots = p.inline_rows && p.n < e ? p.n : e;
-  cut_rows(a, inner, slots, 1);
-  cut_rows(b, b.w.rows, slots, 1);
-  if (slots * a.row_blocks >= ((int64_t)1 << 31) || slots * b.row_blocks >= ((int64_t)1 << 31))
-    return FP4_E_SHAPE;
+  // rows of x in reach of 31 bits; wide strides leave few
+  int64_t most = (kSliceBytes / 2 - gate_up->cols) / x_stride + 1;
+  most = most < p.tokens ? most : p.tokens;
   hipError_t err = hipSuccess;
-  if (!p.inline_rows)
-    err = launch(expert_plan_kernel, (unsigned)e, kPlanThreads, st, experts, (int)p.n, e,
-                 (int32_t*)(base + p.off), (int32_t*)(base + p.order));
-  auto both = [&](auto nt, auto src) {
-    constexpr int N = decltype(nt)::value, S = decltype(src)::value;
-    err = first(err, launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
-    err = first(err, launch_cols<N, 1, false, S>(down->format, b, slots, st));
-  };
-  auto with = [&](auto src) {
-    if (p.n <= 16 * (int64_t)e) both(std::integral_constant<int, 1>{}, src);
-    else both(std::integral_constant<int, 4>{}, src);
-  };
-  if (p.inline_rows) with(std::integral_constant<int, kInline>{});
-  else with(std::integral_constant<int, kPlanned>{});
-  const int64_t quads = tokens * (down->rows / 4);
-  if (cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
-  err = first(err, launch(experts_join_kernel, (unsigned)cdiv(quads, kJoinThreads), kJoinThreads, st,
-                          (const float*)(base + p.y), weights, experts, tokens, (int)top_k, e,
-                          (int)down->rows, out, out_stride));
+  for (int64_t t = 0; t < tokens && err == hipSuccess; t += most)
+    err = experts_slice(gate_up, down, p, x + t * x_stride, x_stride,
+                        tokens - t < most ? tokens - t : most, weights + t * top_k,
+                        experts + t * top_k, (int)top_k, out + t * out_stride, out_stride,
+                        (uint8_t*)ws, (hipStream_t)stream);
   return launched(err);
 }
 

@@ -424,9 +424,9 @@ typedef struct {
   const uint8_t* scales;       /* 2-byte aligned                              */
   const float* alpha;          /* 4-byte aligned                              */
   int64_t experts;             /* 1 for a plain matrix                        */
-  int64_t rows, cols;          /* below 2^24; cols a multiple of 32, rows of 16
-                                  with FP4_BLOCK2D; experts x rows x cols at
-                                  most 2^40                                   */
+  int64_t rows, cols;          /* below 2^24 and 2^22; cols a multiple of 32,
+                                  rows of 16 with FP4_BLOCK2D; experts x rows
+                                  x cols at most 2^40                         */
   int32_t format;              /* FP4_FORMAT_NVFP4 or FP4_FORMAT_MXFP4        */
   uint32_t flags;              /* NVFP4: FP4_BLOCK2D, FP4_ROW_ALPHA; MXFP4: 0 */
 } fp4_weights;
@@ -452,15 +452,16 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
  * index first), each with
  *   weight = scale s_i, or with renormalize  scale s_i / sum of the chosen s.
  * Places without a candidate get expert -1 and weight 0.  A NaN or +inf among
- * softmax's logits makes the weights of its token NaN. */
+ * softmax's logits makes the weights of its chosen experts NaN. */
 typedef struct {
   const void* logits;          /* fp32 or bf16, aligned to its elements       */
   int64_t stride;              /* elements between tokens, at least experts   */
   int64_t tokens;
   const float* bias;           /* [experts] or NULL                           */
   int32_t experts, top_k;      /* 1 to 1024; 1 to 64 and at most experts      */
-  int32_t groups, top_groups;  /* groups divide the experts; top_groups of
-                                  them hold top_k experts at least            */
+  int32_t groups, top_groups;  /* up to 64 groups, dividing the experts;
+                                  top_groups of them hold top_k experts at
+                                  least                                       */
   int32_t group_top;           /* 1 or 2                                      */
   int32_t sigmoid;             /* 0: softmax                                  */
   int32_t renormalize;
@@ -487,8 +488,8 @@ size_t fp4_experts_workspace_bytes(const fp4_weights* gate_up, const fp4_weights
  * [experts][2F][cols], down D_e [experts][cols][F].  The hidden values are
  * rounded to bf16 between the products, sums and the rest are fp32.  Numbers
  * outside [0, experts) are skipped; a token without an expert gets 0; an expert
- * named twice counts twice.  tokens x top_k below 2^31 / 16, experts up to
- * 1024.  out may not overlap x.  Equal calls give equal bits. */
+ * named twice counts twice.  Up to 1024 experts, 64 a token.  out may not
+ * overlap x.  Equal calls give equal bits. */
 int fp4_experts(const fp4_weights* gate_up, const fp4_weights* down, const uint16_t* x,
                 int64_t x_stride, int64_t tokens, const float* weights, const int32_t* experts,
                 int64_t top_k, uint16_t* out, int64_t out_stride, void* ws, size_t ws_bytes,

@@ -32,12 +32,12 @@ WEIGHTS_BAD = [
     (dict(codes=None), E_NULL), (dict(scales=None), E_NULL), (dict(alpha=None), E_NULL),
     (dict(codes=P + 8), E_ALIGN), (dict(scales=P + 1), E_ALIGN), (dict(alpha=F4 + 2), E_ALIGN),
     (dict(rows=-1), E_SHAPE), (dict(cols=-32), E_SHAPE), (dict(cols=80), E_SHAPE),
-    (dict(experts=-1), E_SHAPE), (dict(rows=1 << 24), E_SHAPE), (dict(cols=1 << 24), E_SHAPE),
+    (dict(experts=-1), E_SHAPE), (dict(rows=1 << 24), E_SHAPE), (dict(cols=1 << 22), E_SHAPE),
     (dict(format=2), E_FLAGS), (dict(format=-1), E_FLAGS), (dict(flags=fp4.RHT16), E_FLAGS),
     (dict(flags=fp4.HAD32), E_FLAGS), (dict(format=fp4.FORMAT_MXFP4, flags=fp4.ROW_ALPHA), E_FLAGS),
     (dict(format=fp4.FORMAT_MXFP4, flags=fp4.BLOCK2D), E_FLAGS),
     (dict(flags=fp4.BLOCK2D, rows=72), E_SHAPE),
-    (dict(experts=1 << 24, rows=1 << 20, cols=1 << 20), E_SHAPE),
+    (dict(experts=1 << 20, rows=1 << 20, cols=1 << 20), E_SHAPE),
 ]
 
 
@@ -106,8 +106,8 @@ def test_experts_reject(L):
     assert experts(L, *many) == E_SHAPE
     assert experts(L, gu, dn, tokens=-1) == E_SHAPE
     assert experts(L, gu, dn, k=0) == E_SHAPE
-    assert experts(L, gu, dn, tokens=1 << 27, k=1) == E_SHAPE
-    assert experts(L, gu, dn, tokens=1 << 26, k=2) == E_SHAPE
+    assert experts(L, gu, dn, k=65) == E_SHAPE
+    assert experts(L, gu, dn, tokens=1 << 31) == E_SHAPE
     assert experts(L, gu, dn, xs=88) == E_SHAPE
     assert experts(L, gu, dn, os_=100) == E_SHAPE
     assert experts(L, gu, dn, x=P + 8) == E_ALIGN
