@@ -12,6 +12,7 @@
 #include "experts_kernels.h"
 #include "host_common.h"
 #include "linear_kernels.h"
+#include "linear_stream_kernels.h"
 #include "linear_tiled_kernels.h"
 #include "residual_kernels.h"
 #include "route_kernels.h"
@@ -52,6 +53,9 @@ inline WeightView weight_view(const fp4_weights* w) {
   return v;
 }
 
+// The kernels address rows of x in 31 bits: 128 of them stay within.
+constexpr int64_t kMaxXStride = (int64_t)1 << 23;
+
 // Rows of `width` elements, `stride` apart.
 inline int check_rows(int64_t tokens, int64_t stride, int64_t width, int64_t multiple) {
   if (stride < width || stride % multiple || stride >= kMaxElems) return FP4_E_SHAPE;
@@ -61,21 +65,56 @@ inline int check_rows(int64_t tokens, int64_t stride, int64_t width, int64_t mul
 // ------------------------------------------------------------------ few tokens
 // Waves that share a row's K, the fewest that give every CU two workgroups (or
 // have a step of K each): fewer meet in fewer joins.
-inline void cut_rows(ColsArgs& a, int rows, int64_t slots, int r) {
+inline void cut_rows(ColsArgs& a, int rows, int64_t slots, int r, int waves) {
   const int steps = (a.w.cols + kColsStep - 1) / kColsStep;
   a.wk = 1;
-  while (a.wk < kColsWaves && a.wk < steps &&
-         cdiv(rows, 16 * r * (kColsWaves / a.wk)) * slots < 2 * num_cus())
+  while (a.wk < waves && a.wk < steps && cdiv(rows, 16 * r * (waves / a.wk)) * slots * waves < 16 * num_cus())
     a.wk *= 2;
-  a.row_blocks = (int)cdiv(rows, 16 * r * (kColsWaves / a.wk));
+  a.row_blocks = (int)cdiv(rows, 16 * r * (waves / a.wk));
 }
 
 template <int NT, int R, bool GATED, int SRC>
-hipError_t launch_cols(int format, const ColsArgs& a, int64_t slots, hipStream_t st) {
-  const unsigned grid = (unsigned)(slots * a.row_blocks);
+hipError_t launch_cols(int format, ColsArgs a, int64_t slots, hipStream_t st) {
+  constexpr int W = SRC == kDense ? 8 : 4;
+  cut_rows(a, GATED ? a.inner : a.w.rows, slots, R, W);
+  const int64_t grid = slots * a.row_blocks;
+  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
   return format == FP4_FORMAT_NVFP4
-             ? launch(fp4_cols_kernel<0, NT, R, GATED, SRC>, grid, kColsThreads, st, a)
-             : launch(fp4_cols_kernel<1, NT, R, GATED, SRC>, grid, kColsThreads, st, a);
+             ? launch(fp4_cols_kernel<0, NT, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a)
+             : launch(fp4_cols_kernel<1, NT, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a);
+}
+
+// Streams of codes read scales in whole dwords.
+inline bool stream_fits(const fp4_weights* w) {
+  return w->cols % (w->format == FP4_FORMAT_NVFP4 ? 64 : 128) == 0 && aligned(w->scales, 4);
+}
+
+// busy: workgroups' worth of experts that can have tokens; tokens: an upper bound
+// of an expert's.  Where rows are few their K is cut until every CU has a
+// workgroup.  Where they are many a workgroup takes several blocks, up to four
+// rounds of workgroups, since experts have unequal numbers of tokens (64 tokens
+// through 128 experts, gate and up: 1 round 161 us, 2 131, 4 120, 8 120).
+template <bool GATED, int SRC>
+hipError_t launch_stream(int format, ColsArgs a, int64_t slots, int64_t busy, int64_t tokens,
+                         hipStream_t st) {
+  const int64_t rows = GATED ? a.inner : a.w.rows, wave_rows = GATED ? 16 : 32;
+  int shift = 9;                         // of a segment: as much as fits, at most all of K
+  const int64_t cols = tokens < 16 ? tokens : 16;
+  while ((cols << (shift + 2)) <= kStreamX && (1 << shift) < a.w.cols) shift++;
+  a.kseg_shift = shift;
+  a.wk = 1;
+  while (a.wk < kStreamWaves && 1024 * a.wk <= (1 << shift) && 512 * a.wk < a.w.cols &&
+         cdiv(rows, wave_rows * (kStreamWaves / a.wk)) * busy < num_cus())
+    a.wk *= 2;
+  const int64_t all = cdiv(rows, wave_rows * (kStreamWaves / a.wk));
+  const int64_t each = a.wk == 1 ? all * busy / (8 * num_cus()) : 1;
+  a.blocks = (int)(each < 1 ? 1 : (each < all ? each : all));
+  a.row_blocks = (int)cdiv(all, a.blocks);
+  const int64_t grid = slots * a.row_blocks;
+  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  return format == FP4_FORMAT_NVFP4
+             ? launch(fp4_stream_kernel<0, GATED, SRC>, (unsigned)grid, kStreamThreads, st, a)
+             : launch(fp4_stream_kernel<1, GATED, SRC>, (unsigned)grid, kStreamThreads, st, a);
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -105,11 +144,19 @@ inline TiledArgs tiled_args(const ColsArgs& a) {
   t.experts = a.experts;
   t.inner = a.inner;
   t.x_per_token = a.x_per_token;
+  t.x_bytes = a.x_bytes;
   t.out_f32 = a.out_f32;
   return t;
 }
 
-inline int linear_tiles(int64_t tokens) { return tokens <= 16 ? 1 : (tokens <= 32 ? 2 : 4); }
+// Tiles of 16 tokens that a workgroup takes.
+inline int linear_tiles(int64_t tokens) { return tokens < 64 ? (int)cdiv(tokens, 16) : 4; }
+
+// Row tiles of a wave: four, so that a token's activations are read for 64 rows
+// at a time, where that leaves work for three CUs of four.
+inline bool tall(int64_t rows, int64_t slots, int r) {
+  return cdiv(rows, 16 * r) * slots * 4 >= 3 * (int64_t)num_cus();
+}
 
 // ------------------------------------------------------------------ experts
 // The tiled kernel addresses its rows of x and h in 31 bits: batches past that
@@ -185,21 +232,36 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
   b.os = down->rows;
   b.out_f32 = 1;
   b.x_per_token = 0;
+  a.x_bytes = ((tokens - 1) * x_stride + gate_up->cols) * 2;
+  b.x_bytes = n * inner * 2;
   const int64_t slots = p.inline_rows && n < e ? n : e;
-  cut_rows(a, inner, slots, 1);
-  cut_rows(b, b.w.rows, slots, 1);
   const int64_t quads = tokens * (down->rows / 4);
-  if (slots * a.row_blocks >= ((int64_t)1 << 31) || slots * b.row_blocks >= ((int64_t)1 << 31) ||
-      cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31))
-    return hipErrorInvalidConfiguration;
+  if (cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
   hipError_t err = hipSuccess;
   if (!p.inline_rows)
     err = launch(expert_plan_kernel, (unsigned)e, kPlanThreads, st, experts, (int)n, e,
                  (int32_t*)(ws + p.off), (int32_t*)(ws + p.order));
+  if (tokens <= 16 && n <= kFewMost && stream_fits(down)) {
+    if (stream_fits(gate_up))
+      err = launch_stream<true, kInline>(gate_up->format, a, slots, slots < e ? slots : e, tokens, st);
+    else
+      err = launch_cols<1, 1, true, kInline>(gate_up->format, a, slots, st);
+    b.out = out;
+    b.os = out_stride;
+    const unsigned grid = (unsigned)cdiv(b.w.rows, 16);
+    return first(err, down->format == FP4_FORMAT_NVFP4
+                          ? launch(fp4_down_few_kernel<0>, grid, kFewThreads, st, b, weights)
+                          : launch(fp4_down_few_kernel<1>, grid, kFewThreads, st, b, weights));
+  }
   auto both = [&](auto nt, auto src) {
     constexpr int N = decltype(nt)::value, S = decltype(src)::value;
-    err = first(err, launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
-    err = first(err, launch_cols<N, 1, false, S>(down->format, b, slots, st));
+    const int64_t busy = slots < e ? slots : e;      // experts that can have tokens
+    err = first(err, stream_fits(gate_up)
+                         ? launch_stream<true, S>(gate_up->format, a, slots, busy, tokens, st)
+                         : launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
+    err = first(err, stream_fits(down)
+                         ? launch_stream<false, S>(down->format, b, slots, busy, tokens, st)
+                         : launch_cols<N, 2, false, S>(down->format, b, slots, st));
   };
   auto with = [&](auto src) {
     if (n <= 16 * (int64_t)e) both(std::integral_constant<int, 1>{}, src);
@@ -209,8 +271,6 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
     TiledArgs ta = tiled_args(a), tb = tiled_args(b);
     ta.tiles_t = tb.tiles_t = (uint32_t)(n / kTileTokens + e);
     ta.out_vec = tb.out_vec = 1;
-    ta.x_bytes = ((tokens - 1) * x_stride + gate_up->cols) * 2;
-    tb.x_bytes = n * inner * 2;
     err = first(err, launch_tiled<true, true>(gate_up->format, ta, st));
     err = first(err, launch_tiled<false, true>(down->format, tb, st));
   } else if (p.inline_rows) {
@@ -342,6 +402,7 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
   if (tokens == 0 || w->rows == 0) return FP4_OK;
   if ((!x && w->cols) || !out) return FP4_E_NULL;
   if (int rc = check_rows(tokens, x_stride, w->cols, 8)) return rc;
+  if (x_stride >= kMaxXStride) return FP4_E_SHAPE;
   if (int rc = check_rows(tokens, out_stride, w->rows, 1)) return rc;
   if (!aligned(x, 16) || !aligned(out, out_f32 ? 4 : 2)) return FP4_E_ALIGN;
   ColsArgs a = {};
@@ -353,22 +414,28 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
   a.tokens = tokens;
   a.out_f32 = out_f32 != 0;
   a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
-  if (tokens > 128 && cdiv(tokens, kTileTokens) * cdiv(w->rows, kTileWeights) >= 64 && w->cols > 0 &&
-      (kTileTokens * x_stride + w->cols) * 2 <= kSliceBytes) {
+  if (tokens > 128 && cdiv(tokens, kTileTokens) * cdiv(w->rows, kTileWeights) >= 64 && w->cols > 0) {
     TiledArgs t = tiled_args(a);
     t.tiles_t = (uint32_t)cdiv(tokens, kTileTokens);
     t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
     return launched(launch_tiled<false, false>(w->format, t, (hipStream_t)stream));
   }
+  if (tokens <= 16 && w->rows >= 8192 && stream_fits(w))
+    return launched(launch_stream<false, kDense>(w->format, a, 1, 1, tokens, (hipStream_t)stream));
   const int nt = linear_tiles(tokens);
   const int64_t slots = cdiv(tokens, 16 * nt);
-  cut_rows(a, a.w.rows, slots, 1);
-  if (slots * a.row_blocks >= ((int64_t)1 << 31)) return FP4_E_SHAPE;
   hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    constexpr int R = N == 1 ? 2 : 4;
+    return tall(w->rows, slots, R) ? launch_cols<N, R, false, kDense>(w->format, a, slots, st)
+                                   : launch_cols<N, 1, false, kDense>(w->format, a, slots, st);
+  };
   switch (nt) {
-    case 1: return launched(launch_cols<1, 1, false, kDense>(w->format, a, slots, st));
-    case 2: return launched(launch_cols<2, 1, false, kDense>(w->format, a, slots, st));
-    default: return launched(launch_cols<4, 1, false, kDense>(w->format, a, slots, st));
+    case 1: return launched(go(std::integral_constant<int, 1>{}));
+    case 2: return launched(go(std::integral_constant<int, 2>{}));
+    case 3: return launched(go(std::integral_constant<int, 3>{}));
+    default: return launched(go(std::integral_constant<int, 4>{}));
   }
 }
 
@@ -438,13 +505,14 @@ int fp4_experts(const fp4_weights* gate_up, const fp4_weights* down, const uint1
   if (tokens == 0) return FP4_OK;
   if (!x || !weights || !experts || !out || !ws) return FP4_E_NULL;
   if (int rc = check_rows(tokens, x_stride, gate_up->cols, 8)) return rc;
+  if (x_stride >= kMaxXStride) return FP4_E_SHAPE;
   if (int rc = check_rows(tokens, out_stride, gate_up->cols, 8)) return rc;
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(weights, 4) || !aligned(experts, 4) ||
       !aligned(ws, 16))
     return FP4_E_ALIGN;
   const ExpertsPlan p = experts_plan(gate_up, down, tokens, top_k);
   if (ws_bytes < p.bytes) return FP4_E_WORKSPACE;
-  // rows of x in reach of 31 bits; wide strides leave few
+  // rows of x in reach of 31 bits
   int64_t most = (kSliceBytes / 2 - gate_up->cols) / x_stride + 1;
   most = most < p.tokens ? most : p.tokens;
   hipError_t err = hipSuccess;

@@ -101,15 +101,15 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
     count = a.tokens - first < kTileTokens ? a.tokens - first : kTileTokens;
     tn = (uint32_t)to.tx;
   }
+  const float all = alpha_all(a.w, e);
   const int rows = GATED ? a.inner : a.w.rows, K = a.w.cols;
   constexpr int WAVE_ROWS = GATED ? 32 : 64;
   const int n0 = (int)tn * (GATED ? kTileWeights / 2 : kTileWeights) + wave * WAVE_ROWS;
 
-  // Buffers over the tile's rows of weights and over x: what lies past them or
-  // past K is read as zeros, and zero times zero adds nothing.  Offsets of a
-  // lane's row in them, values past 2^31 excluded by the host.
+  // Buffers over the tile's rows of weights and over x: what lies past them, or
+  // past K, is read as zeros, and zero times zero adds nothing.  The host keeps
+  // all offsets under 2^31.
   constexpr int G = WeightFmt<FMT>::G;
-  constexpr uint32_t kOob = 0x7FFFFF00u;
   const int row0 = (int)tn * (GATED ? kTileWeights / 2 : kTileWeights);
   __amdgpu_buffer_rsrc_t rc[GATED ? 2 : 1], rs[GATED ? 2 : 1];
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
       row = a.order[first + (t < count ? t : 0)];
       if (a.x_per_token) row = (int64_t)((uint32_t)row / (uint32_t)a.top_k);
     }
-    xoff[i] = t < count ? (uint32_t)(row * a.xs * 2) + 16 * ((lane & 15) ^ (t & 15)) : kOob;
+    xoff[i] = t < count ? (uint32_t)(row * a.xs * 2) + 16 * ((lane & 15) ^ (t & 15)) : kBufferEnd;
   }
 
   auto fill = [&](uint8_t* buf, int ks) {
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
       const int chunk = (lane & 15) ^ ((4 * i + (lane >> 4)) & 15);
       const bool in = ks * kTileK + 8 * chunk < K;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(buf + 1024 * (8 * wave + i)), 16,
-                                               in ? xoff[i] + ks * (2 * kTileK) : kOob, 0, 0, 0);
+                                               in ? xoff[i] + ks * (2 * kTileK) : kBufferEnd, 0, 0, 0);
     }
   };
   auto load_codes = [&](StageCodes<FMT>& c, int ks) {
@@ -158,8 +158,8 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
 #pragma unroll
       for (int s = 0; s < 2; s++) {
         const bool in = k0 + 64 * hh + 32 * s < K;
-        const int co = (int)(in ? coff[i] + k0 / 2 + 16 * s : kOob);
-        const int so = (int)(in ? soff[i] + (k0 + 32 * s) / G : kOob);
+        const int co = (int)(in ? coff[i] + k0 / 2 + 16 * s : kBufferEnd);
+        const int so = (int)(in ? soff[i] + (k0 + 32 * s) / G : kBufferEnd);
         c.c[i][s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rc[GATED ? i : 0], co, 0, 0));
         if constexpr (FMT == 0) b[s] = __builtin_amdgcn_raw_buffer_load_b16(rs[GATED ? i : 0], so, 0, 0);
         else b[s] = __builtin_amdgcn_raw_buffer_load_b8(rs[GATED ? i : 0], so, 0, 0);
@@ -257,8 +257,8 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
 #pragma unroll
       for (int v = 0; v < 16; v++) {
         const int n = nb + 8 * (v / 4) + 4 * hh + v % 4, row = n < rows ? n : rows - 1;
-        y[v] = acc[i][j][v] * alpha_of(a.w, e, row);
-        if constexpr (GATED) y[v] = silu_times(y[v], acc[1][j][v] * alpha_of(a.w, e, row + rows));
+        y[v] = acc[i][j][v] * alpha_row(a.w, e, row, all);
+        if constexpr (GATED) y[v] = silu_times(y[v], acc[1][j][v] * alpha_row(a.w, e, row + rows, all));
       }
       if (a.out_f32) {
         if (c >= count) continue;

@@ -28,6 +28,9 @@ struct WeightView {
   int row_alpha;                         // floats from one row's alpha to the next (0 or 1)
 };
 
+// An offset past every buffer here (they end below it): reads as zeros.
+constexpr uint32_t kBufferEnd = 0x7FFFFF00u;
+
 // FMT: FP4_FORMAT_NVFP4 (0) or FP4_FORMAT_MXFP4 (1).
 template <int FMT>
 struct WeightFmt {
@@ -44,8 +47,13 @@ template <int FMT>
 __device__ __forceinline__ const uint8_t* scale_row(const WeightView& w, int64_t e, int n) {
   return w.scales + e * w.scales_e + (int64_t)(n >> w.tile_shift) * (w.cols / WeightFmt<FMT>::G);
 }
-__device__ __forceinline__ float alpha_of(const WeightView& w, int64_t e, int n) {
-  return w.alpha ? w.alpha[e * w.alpha_e + (int64_t)n * w.row_alpha] : 1.0f;
+// An expert's alpha where it is one number, loaded early and by the scalar unit.
+__device__ __forceinline__ float alpha_all(const WeightView& w, int64_t e) {
+  return w.alpha && !w.row_alpha ? w.alpha[e * w.alpha_e] : 1.0f;
+}
+// A row's factor, all = alpha_all.
+__device__ __forceinline__ float alpha_row(const WeightView& w, int64_t e, int n, float all) {
+  return w.row_alpha ? w.alpha[e * w.alpha_e + n] : all;
 }
 
 // The scale bytes of the 32 codes from k on (k a multiple of 32).
@@ -90,6 +98,18 @@ __device__ __forceinline__ u32x4_t decode8(uint32_t w, float s) {
 __device__ __forceinline__ f32x4_t mfma16_bf16(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Wait until at most N of this wave's vector-memory operations are under way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
+}
+// Wait for this wave's LDS operations.
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
 }
 
 // silu(g) u.  The exponential overflows to infinity below -88: silu is -0 there.

@@ -402,7 +402,8 @@ int qk_norm_rope_backward(const fp4_qk_rope* x, const uint16_t* dq_out, int64_t 
  *
  * Activations are bf16 [tokens][cols]; `*_stride` is the number of elements
  * from one row to the next, at least the row's length and (but for the
- * outputs of fp4_linear) a multiple of 8.  Pointers are 16-byte aligned where
+ * outputs of fp4_linear) a multiple of 8; that of x in fp4_linear and
+ * fp4_experts is below 2^23.  Pointers are 16-byte aligned where
  * nothing else is said.  The structs are read by the call itself and need not
  * outlive it.
  * ------------------------------------------------------------------------ */

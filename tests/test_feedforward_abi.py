@@ -64,6 +64,7 @@ def test_linear_rejects(L):
     assert linear(L, w, xs=100) == E_SHAPE           # not a multiple of 8
     assert linear(L, w, os_=63) == E_SHAPE
     assert linear(L, w, xs=1 << 39) == E_SHAPE
+    assert linear(L, w, xs=1 << 23) == E_SHAPE
     assert linear(L, w, x=P + 8) == E_ALIGN
     assert linear(L, w, out=P + 1) == E_ALIGN
     assert linear(L, w, out=P + 2, f32=1) == E_ALIGN
@@ -110,6 +111,7 @@ def test_experts_reject(L):
     assert experts(L, gu, dn, tokens=1 << 31) == E_SHAPE
     assert experts(L, gu, dn, xs=88) == E_SHAPE
     assert experts(L, gu, dn, os_=100) == E_SHAPE
+    assert experts(L, gu, dn, xs=1 << 23) == E_SHAPE
     assert experts(L, gu, dn, x=P + 8) == E_ALIGN
     assert experts(L, gu, dn, out=P + 8) == E_ALIGN
     assert experts(L, gu, dn, ids=F4 + 2) == E_ALIGN
