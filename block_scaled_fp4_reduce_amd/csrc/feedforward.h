@@ -315,18 +315,43 @@ inline RouteArgs route_args(const fp4_routing* r) {
   a.top_groups = r->top_groups;
   a.group_top = r->group_top;
   a.renormalize = r->renormalize;
+  a.sigmoid = r->sigmoid != 0;
   a.scale = r->scale;
   return a;
 }
 
-// f(values a lane) with that as a compile-time constant.
+// Sixteen lanes a token where they hold its experts, 16 each, and its choices and
+// one more.
+inline bool route_narrow(const RouteArgs& a) { return a.experts <= 256 && a.top_k <= 15; }
+
+// Experts of a lane, so that a group is a run of 2^i lanes; false if none fits.
+inline bool route_lanes(RouteArgs& a, int lanes, int most) {
+  a.per_lane = most;
+  a.group_lanes = 1;
+  if (a.groups <= 1) return true;
+  const int per = a.experts / a.groups;
+  for (int run = 1; run * a.groups <= lanes && per % run == 0; run *= 2)
+    if (per / run <= most) {
+      a.per_lane = per / run;
+      a.group_lanes = run;
+      return true;
+    }
+  return false;
+}
+
+// f(lanes a token, values a lane) as compile-time constants.
 template <typename F>
-hipError_t route_variant(int experts, F&& f) {
-  if (experts <= 64) return f(std::integral_constant<int, 1>{});
-  if (experts <= 128) return f(std::integral_constant<int, 2>{});
-  if (experts <= 256) return f(std::integral_constant<int, 4>{});
-  if (experts <= 512) return f(std::integral_constant<int, 8>{});
-  return f(std::integral_constant<int, 16>{});
+hipError_t route_variant(const RouteArgs& a, F&& f) {
+  using std::integral_constant;
+  if (route_narrow(a)) {
+    const integral_constant<int, 16> l;
+    if (a.experts <= 64) return f(l, integral_constant<int, 4>{});
+    if (a.experts <= 128) return f(l, integral_constant<int, 8>{});
+    return f(l, integral_constant<int, 16>{});
+  }
+  const integral_constant<int, 64> l;
+  if (a.experts <= 256) return f(l, integral_constant<int, 4>{});
+  return f(l, integral_constant<int, 16>{});
 }
 
 // ------------------------------------------------------------------ norms around a block
@@ -447,20 +472,18 @@ int expert_route(const fp4_routing* r, float* weights, int32_t* experts, void* s
   if (r->tokens == 0) return FP4_OK;
   if (!weights || !experts) return FP4_E_NULL;
   if (!aligned(weights, 4) || !aligned(experts, 4)) return FP4_E_ALIGN;
-  const RouteArgs a = route_args(r);
-  const unsigned grid = (unsigned)cdiv(a.tokens, kRouteWaves);
-  const bool wide = a.bias || (a.groups > 1 && a.group_top == 2);
-  return launched(route_variant(a.experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    auto go = [&](auto kernel) {
-      return launch(kernel, grid, kRouteThreads, (hipStream_t)stream, a, (int)(r->sigmoid != 0),
-                    weights, experts);
+  RouteArgs a = route_args(r);
+  return launched(route_variant(a, [&](auto lpt, auto v) {
+    constexpr int L = decltype(lpt)::value, V = decltype(v)::value, V64 = (L * V + 63) / 64;
+    auto go = [&](auto kernel, int tokens) {
+      return launch(kernel, (unsigned)cdiv(a.tokens, kRouteWaves * tokens), kRouteThreads,
+                    (hipStream_t)stream, a, weights, experts);
     };
-    if (wide)
-      return r->logits_bf16 ? go(expert_route_kernel<double, V, true>)
-                            : go(expert_route_kernel<double, V, false>);
-    return r->logits_bf16 ? go(expert_route_kernel<float, V, true>)
-                          : go(expert_route_kernel<float, V, false>);
+    if (!route_lanes(a, L, V) || a.top_k >= L)
+      return r->logits_bf16 ? go(expert_route64_kernel<V64, true>, 1)
+                            : go(expert_route64_kernel<V64, false>, 1);
+    return r->logits_bf16 ? go(expert_route_kernel<L, V, true>, 64 / L)
+                          : go(expert_route_kernel<L, V, false>, 64 / L);
   }));
 }
 
@@ -476,15 +499,14 @@ int expert_route_backward(const fp4_routing* r, const float* dweights, const int
     return FP4_E_ALIGN;
   RouteArgs a = route_args(r);
   a.bias = nullptr;
-  const unsigned grid = (unsigned)cdiv(a.tokens, kRouteWaves);
-  return launched(route_variant(a.experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
+  return launched(route_variant(a, [&](auto lpt, auto v) {
+    constexpr int L = decltype(lpt)::value, V = decltype(v)::value;
     auto go = [&](auto kernel) {
-      return launch(kernel, grid, kRouteThreads, (hipStream_t)stream, a, (int)(r->sigmoid != 0),
-                    dweights, experts, dlogits, dlogits_stride);
+      return launch(kernel, (unsigned)cdiv(a.tokens, kRouteWaves * (64 / L)), kRouteThreads,
+                    (hipStream_t)stream, a, dweights, experts, dlogits, dlogits_stride);
     };
-    return r->logits_bf16 ? go(expert_route_backward_kernel<V, true>)
-                          : go(expert_route_backward_kernel<V, false>);
+    return r->logits_bf16 ? go(expert_route_backward_kernel<L, V, true>)
+                          : go(expert_route_backward_kernel<L, V, false>);
   }));
 }
 
