@@ -73,15 +73,15 @@ inline void cut_rows(ColsArgs& a, int rows, int64_t slots, int r, int waves) {
   a.row_blocks = (int)cdiv(rows, 16 * r * (waves / a.wk));
 }
 
-template <int NT, int R, bool GATED, int SRC>
+template <int R, bool GATED, int SRC>
 hipError_t launch_cols(int format, ColsArgs a, int64_t slots, hipStream_t st) {
   constexpr int W = SRC == kDense ? 8 : 4;
   cut_rows(a, GATED ? a.inner : a.w.rows, slots, R, W);
   const int64_t grid = slots * a.row_blocks;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
   return format == FP4_FORMAT_NVFP4
-             ? launch(fp4_cols_kernel<0, NT, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a)
-             : launch(fp4_cols_kernel<1, NT, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a);
+             ? launch(fp4_cols_kernel<0, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a)
+             : launch(fp4_cols_kernel<1, R, GATED, SRC, W>, (unsigned)grid, W * 64, st, a);
 }
 
 // Streams of codes read scales in whole dwords.
@@ -117,6 +117,20 @@ hipError_t launch_stream(int format, ColsArgs a, int64_t slots, int64_t busy, in
              : launch(fp4_stream_kernel<1, GATED, SRC>, (unsigned)grid, kStreamThreads, st, a);
 }
 
+// 16 NT tokens at a time; waves share rows where a workgroup's 256 leave CUs idle.
+template <int NT>
+hipError_t launch_mid(int format, ColsArgs a, hipStream_t st) {
+  const int64_t slots = cdiv(a.tokens, 16 * NT);
+  a.wk = 1;
+  while (a.wk < 4 && cdiv(a.w.rows, 32 * (kMidWaves / a.wk)) * slots < num_cus()) a.wk *= 2;
+  a.row_blocks = (int)cdiv(a.w.rows, 32 * (kMidWaves / a.wk));
+  const int64_t grid = slots * a.row_blocks;
+  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  return format == FP4_FORMAT_NVFP4
+             ? launch(fp4_mid_kernel<0, NT>, (unsigned)grid, kMidThreads, st, a)
+             : launch(fp4_mid_kernel<1, NT>, (unsigned)grid, kMidThreads, st, a);
+}
+
 // ------------------------------------------------------------------ many tokens
 template <bool GATED, bool EXPERTS>
 hipError_t launch_tiled(int format, TiledArgs a, hipStream_t st) {
@@ -149,13 +163,27 @@ inline TiledArgs tiled_args(const ColsArgs& a) {
   return t;
 }
 
-// Tiles of 16 tokens that a workgroup takes.
-inline int linear_tiles(int64_t tokens) { return tokens < 64 ? (int)cdiv(tokens, 16) : 4; }
+// Tiles of 16 tokens that a workgroup takes: the fewest with which all workgroups
+// of 64 rows run at once, for the shorter way of each; past that as many as fit.
+inline int linear_tiles(int64_t tokens, int64_t rows) {
+  for (int nt = 1; nt < 4; nt++)
+    if (cdiv(tokens, 16 * nt) * cdiv(rows, 64) <= num_cus()) return nt;
+  return 4;
+}
 
-// Row tiles of a wave: four, so that a token's activations are read for 64 rows
-// at a time, where that leaves work for three CUs of four.
-inline bool tall(int64_t rows, int64_t slots, int r) {
-  return cdiv(rows, 16 * r) * slots * 4 >= 3 * (int64_t)num_cus();
+// Two row tiles a wave, so that a token's activations are read for 32 rows at a
+// time, where that leaves work for three CUs of four.
+inline bool tall(int64_t rows, int64_t slots) {
+  return cdiv(rows, 32) * slots * 4 >= 3 * (int64_t)num_cus();
+}
+
+// A round of 128x256 tiles takes as long as six and a half of 64 tokens x 64 rows
+// (88 us and 13.5 with 4096 columns, whose tiles decode their weights for twice
+// the tokens but wait for each other): whichever has done sooner.
+inline bool tiles_sooner(int64_t tokens, int64_t rows) {
+  const int64_t tiles = cdiv(tokens, kTileTokens) * cdiv(rows, kTileWeights);
+  const int64_t mids = cdiv(tokens, 64) * cdiv(rows, 64);
+  return tokens > 64 && 13 * cdiv(tiles, num_cus()) <= 2 * cdiv(mids, num_cus());
 }
 
 // ------------------------------------------------------------------ experts
@@ -245,7 +273,7 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
     if (stream_fits(gate_up))
       err = launch_stream<true, kInline>(gate_up->format, a, slots, slots < e ? slots : e, tokens, st);
     else
-      err = launch_cols<1, 1, true, kInline>(gate_up->format, a, slots, st);
+      err = launch_cols<1, true, kInline>(gate_up->format, a, slots, st);
     b.out = out;
     b.os = out_stride;
     const unsigned grid = (unsigned)cdiv(b.w.rows, 16);
@@ -253,19 +281,15 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
                           ? launch(fp4_down_few_kernel<0>, grid, kFewThreads, st, b, weights)
                           : launch(fp4_down_few_kernel<1>, grid, kFewThreads, st, b, weights));
   }
-  auto both = [&](auto nt, auto src) {
-    constexpr int N = decltype(nt)::value, S = decltype(src)::value;
+  auto both = [&](auto src) {
+    constexpr int S = decltype(src)::value;
     const int64_t busy = slots < e ? slots : e;      // experts that can have tokens
     err = first(err, stream_fits(gate_up)
                          ? launch_stream<true, S>(gate_up->format, a, slots, busy, tokens, st)
-                         : launch_cols<N, 1, true, S>(gate_up->format, a, slots, st));
+                         : launch_cols<1, true, S>(gate_up->format, a, slots, st));
     err = first(err, stream_fits(down)
                          ? launch_stream<false, S>(down->format, b, slots, busy, tokens, st)
-                         : launch_cols<N, 2, false, S>(down->format, b, slots, st));
-  };
-  auto with = [&](auto src) {
-    if (n <= 16 * (int64_t)e) both(std::integral_constant<int, 1>{}, src);
-    else both(std::integral_constant<int, 4>{}, src);
+                         : launch_cols<2, false, S>(down->format, b, slots, st));
   };
   if (!p.inline_rows && n > 32 * (int64_t)e) {
     TiledArgs ta = tiled_args(a), tb = tiled_args(b);
@@ -274,9 +298,9 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
     err = first(err, launch_tiled<true, true>(gate_up->format, ta, st));
     err = first(err, launch_tiled<false, true>(down->format, tb, st));
   } else if (p.inline_rows) {
-    with(std::integral_constant<int, kInline>{});
+    both(std::integral_constant<int, kInline>{});
   } else {
-    with(std::integral_constant<int, kPlanned>{});
+    both(std::integral_constant<int, kPlanned>{});
   }
   return first(err, launch(experts_join_kernel, (unsigned)cdiv(quads, kJoinThreads), kJoinThreads, st,
                            (const float*)(ws + p.y), weights, experts, tokens, top_k, e,
@@ -439,28 +463,25 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
   a.tokens = tokens;
   a.out_f32 = out_f32 != 0;
   a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
-  if (tokens > 128 && cdiv(tokens, kTileTokens) * cdiv(w->rows, kTileWeights) >= 64 && w->cols > 0) {
+  hipStream_t st = (hipStream_t)stream;
+  if (w->cols > 0 && tiles_sooner(tokens, w->rows)) {
     TiledArgs t = tiled_args(a);
     t.tiles_t = (uint32_t)cdiv(tokens, kTileTokens);
     t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
-    return launched(launch_tiled<false, false>(w->format, t, (hipStream_t)stream));
+    return launched(launch_tiled<false, false>(w->format, t, st));
   }
   if (tokens <= 16 && w->rows >= 8192 && stream_fits(w))
-    return launched(launch_stream<false, kDense>(w->format, a, 1, 1, tokens, (hipStream_t)stream));
-  const int nt = linear_tiles(tokens);
-  const int64_t slots = cdiv(tokens, 16 * nt);
-  hipStream_t st = (hipStream_t)stream;
-  auto go = [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    constexpr int R = N == 1 ? 2 : 4;
-    return tall(w->rows, slots, R) ? launch_cols<N, R, false, kDense>(w->format, a, slots, st)
-                                   : launch_cols<N, 1, false, kDense>(w->format, a, slots, st);
-  };
-  switch (nt) {
-    case 1: return launched(go(std::integral_constant<int, 1>{}));
-    case 2: return launched(go(std::integral_constant<int, 2>{}));
-    case 3: return launched(go(std::integral_constant<int, 3>{}));
-    default: return launched(go(std::integral_constant<int, 4>{}));
+    return launched(launch_stream<false, kDense>(w->format, a, 1, 1, tokens, st));
+  if (tokens <= 16 || w->cols < kMidLeast) {
+    const int64_t slots = cdiv(tokens, 16);
+    return launched(tall(w->rows, slots) ? launch_cols<2, false, kDense>(w->format, a, slots, st)
+                                         : launch_cols<1, false, kDense>(w->format, a, slots, st));
+  }
+  switch (linear_tiles(tokens, w->rows)) {
+    case 1: return launched(launch_mid<1>(w->format, a, st));
+    case 2: return launched(launch_mid<2>(w->format, a, st));
+    case 3: return launched(launch_mid<3>(w->format, a, st));
+    default: return launched(launch_mid<4>(w->format, a, st));
   }
 }
 

@@ -10,10 +10,13 @@
 // number lane / 16 of 128 of row lane % 16; the four lanes of a row then trade
 // dwords, so that a product takes 32 values in a run and the activations are
 // read in whole 64-byte pieces too (read as the codes lie, 16 bytes of every
-// 64, they take most of the cache's lookups: 64 tokens through 128 experts
-// XXX -> YYY us).
+// 64, they would take most of the cache's lookups).  It is the form for small
+// matrices and few tokens, where a launch's latency is most of the time (1 token
+// through 4096x4096: 5.7 us, of which reading the codes at 4.9 TB/s is 1.9), and
+// for sizes that the others do not take; the streams and tiles of
+// linear_stream_kernels.h and linear_tiled_kernels.h read by neighbouring lanes.
 //
-// A workgroup of 8 waves takes a number of rows and cuts K over its waves
+// A workgroup of 8 waves (experts: 4) takes a number of rows and cuts K over its waves
 // (`wk` of them a row; the others take other rows), which meet in LDS: no
 // workspace and no second launch, and the sum's order depends on sizes alone.
 #pragma once
@@ -37,7 +40,6 @@ struct ColsArgs {
   int wk;                                // waves that share a row's K
   int kseg_shift, blocks;                // streams: log2 of a segment of K, row blocks
   int row_blocks;                        // of a matrix (or of F)
-  int col_groups;                        // SRC 0: groups of tokens
   int out_f32, out_vec;                  // fp32 outputs; 4 of them may be stored at once
   int x_per_token;                       // experts: rows of x are tokens (else assignments)
   int64_t x_bytes;                       // experts: of x
@@ -180,13 +182,12 @@ __device__ __forceinline__ void put_rows(const ColsArgs& a, int64_t e, int rows,
   }
 }
 
-// FMT of the weights, NT tiles of 16 tokens, R tiles of 16 rows (GATED: R pairs
-// of a gate's and an up projection's tile).
-template <int FMT, int NT, int R, bool GATED, int SRC, int W>
-__global__ __launch_bounds__(W * 64, NT == 1 && !GATED ? 4 : 2) void fp4_cols_kernel(ColsArgs a) {
-  constexpr int TR = GATED ? 2 * R : R, TILES = TR * NT;
-  constexpr int BATCH = TILES < 4 ? TILES : 4;       // tiles joined at once
-  __shared__ f32x4_t red[W][BATCH][64];
+// FMT of the weights, R tiles of 16 rows a wave (GATED: R pairs of a gate's and an
+// up projection's tile), 16 tokens at a time.
+template <int FMT, int R, bool GATED, int SRC, int W>
+__global__ __launch_bounds__(W * 64, GATED ? 2 : 4) void fp4_cols_kernel(ColsArgs a) {
+  constexpr int TR = GATED ? 2 * R : R;
+  __shared__ f32x4_t red[W][TR][64];
   __shared__ int lists[SRC == kInline ? W : 1][SRC == kInline ? kInlineMost : 1];
   const int t = (int)threadIdx.x, lane = t & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -195,8 +196,8 @@ __global__ __launch_bounds__(W * 64, NT == 1 && !GATED ? 4 : 2) void fp4_cols_ke
   const int rb = (int)(blockIdx.x - slot * (uint32_t)a.row_blocks);
   int64_t e = 0, first = 0, count;
   if constexpr (SRC == kDense) {
-    first = (int64_t)slot * (16 * NT);
-    count = a.tokens - first < 16 * NT ? a.tokens - first : 16 * NT;
+    first = (int64_t)slot * 16;
+    count = a.tokens - first < 16 ? a.tokens - first : 16;
   } else if constexpr (SRC == kPlanned) {
     e = slot;
     first = a.off[slot];
@@ -264,45 +265,38 @@ __global__ __launch_bounds__(W * 64, NT == 1 && !GATED ? 4 : 2) void fp4_cols_ke
       SRC == kDense ? buffer_rsrc(a.x + first * a.xs, ((count - 1) * a.xs + K) * 2)
                     : buffer_rsrc(a.x, a.x_bytes);
 
-  for (int64_t c0 = 0; c0 < count; c0 += 16 * NT) {
-    uint32_t xoff[NT];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {       // columns past the last repeat it and are dropped
-      const int64_t c = c0 + 16 * j + r;
-      int64_t row = c < count ? c : count - 1;
-      if constexpr (SRC != kDense) {
-        row = SRC == kPlanned ? a.order[first + row] : list[row];
-        if (a.x_per_token) row = (int64_t)((uint32_t)row / (uint32_t)a.top_k);
-      }
-      xoff[j] = (uint32_t)(row * a.xs * 2) + 16 * g;
+  for (int64_t c0 = 0; c0 < count; c0 += 16) {
+    // columns past the last repeat it and are dropped
+    int64_t row = c0 + r < count ? c0 + r : count - 1;
+    if constexpr (SRC != kDense) {
+      row = SRC == kPlanned ? a.order[first + row] : list[row];
+      if (a.x_per_token) row = (int64_t)((uint32_t)row / (uint32_t)a.top_k);
     }
-    f32x4_t acc[TR][NT] = {};
-    auto multiply = [&](const Step& f, int half, const u32x4_t (&x)[NT][4]) {
+    const uint32_t xoff = (uint32_t)(row * a.xs * 2) + 16 * g;
+    f32x4_t acc[TR] = {};
+    auto multiply = [&](const Step& f, int half, const u32x4_t (&x)[4]) {
 #pragma unroll
       for (int i = 0; i < TR; i++) {
         const u32x4_t code = turn_groups(f.code[i][half]);
 #pragma unroll
         for (int q = 0; q < 4; q++) {
           const u32x4_t op = decode8<FMT>(code[q], f.sc[i].at(half, q, g));
-#pragma unroll
-          for (int j = 0; j < NT; j++) acc[i][j] = mfma16_bf16(op, x[j][q], acc[i][j]);
+          acc[i] = mfma16_bf16(op, x[q], acc[i]);
         }
       }
     };
-    auto load_x = [&](u32x4_t (&x)[NT][4], int step, int half) {
+    auto load_x = [&](u32x4_t (&x)[4], int step, int half) {
       const int k0 = place(step) * kColsStep + 128 * half, left = step < steps ? K - k0 : 0;
 #pragma unroll
-      for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int o = 32 * q < left ? (int)xoff[j] + 2 * k0 + 64 * q : (int)kBufferEnd;
-          x[j][q] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, o, 0, 0));
-        }
+      for (int q = 0; q < 4; q++) {
+        const int o = 32 * q < left ? (int)xoff + 2 * k0 + 64 * q : (int)kBufferEnd;
+        x[q] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, o, 0, 0));
+      }
     };
     // Loads come back in their order, so a step's second activations go out
     // before the next step's codes, which have the longest way.
     Step f0, f1;
-    u32x4_t x0[NT][4], x1[NT][4];
+    u32x4_t x0[4], x1[4];
     load_x(x0, kpart, 0);
     load(f0, kpart);
     auto one = [&](Step& f, Step& next, int step) {
@@ -316,34 +310,27 @@ __global__ __launch_bounds__(W * 64, NT == 1 && !GATED ? 4 : 2) void fp4_cols_ke
       one(f0, f1, step);
       one(f1, f0, step + a.wk);
     }
-    // join the waves of a row block: tiles in batches, one value of a lane each
+    // join the waves of a row block, one value of a lane each
+    __syncthreads();
 #pragma unroll
-    for (int b = 0; b < TILES; b += BATCH) {
-      __syncthreads();
+    for (int i = 0; i < TR; i++) red[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int item = t; item < wr * R * 64; item += W * 64) {
+      const int l = item & 63, tile = item / 64 % R, set = item / (64 * R);
+      f32x4_t v[GATED ? 2 : 1];
 #pragma unroll
-      for (int i = 0; i < BATCH; i++)    // tile order: pairs of a gate and an up tile together
-        red[wave][i][lane] = acc[GATED ? 2 * ((b + i) / 2 / NT) + (b + i) % 2 : (b + i) / NT]
-                                [GATED ? (b + i) / 2 % NT : (b + i) % NT];
-      __syncthreads();
-      constexpr int OUT = GATED ? BATCH / 2 : BATCH;
-      for (int item = t; item < wr * OUT * 64; item += W * 64) {
-        const int l = item & 63, tile = item / 64 % OUT, set = item / (64 * OUT);
-        f32x4_t v[GATED ? 2 : 1];
-#pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); h++) {
-          v[h] = red[set * a.wk][GATED ? 2 * tile + h : tile][l];
-          for (int w = 1; w < a.wk; w++)
-            v[h] += red[set * a.wk + w][GATED ? 2 * tile + h : tile][l];
-        }
-        const int at = (GATED ? b / 2 : b) + tile;   // row tile and token tile
-        const int n = blk + set * 16 * R + 16 * (at / NT) + 4 * (l >> 4);
-        const int64_t c = c0 + 16 * (at % NT) + (l & 15);
-        if (c >= count || n >= rows) continue;
-        int64_t orow = c;
-        if constexpr (SRC == kDense) orow += first;
-        else orow = SRC == kPlanned ? a.order[first + c] : list[c];
-        put_rows<GATED>(a, e, rows, n, orow, all, v);
+      for (int h = 0; h < (GATED ? 2 : 1); h++) {
+        const int at = GATED ? 2 * tile + h : tile;
+        v[h] = red[set * a.wk][at][l];
+        for (int w = 1; w < a.wk; w++) v[h] += red[set * a.wk + w][at][l];
       }
+      const int n = blk + set * 16 * R + 16 * tile + 4 * (l >> 4);
+      const int64_t c = c0 + (l & 15);
+      if (c >= count || n >= rows) continue;
+      int64_t orow = c;
+      if constexpr (SRC == kDense) orow += first;
+      else orow = SRC == kPlanned ? a.order[first + c] : list[c];
+      put_rows<GATED>(a, e, rows, n, orow, all, v);
     }
   }
 }

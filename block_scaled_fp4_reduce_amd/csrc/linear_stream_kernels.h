@@ -269,6 +269,221 @@ __global__ __launch_bounds__(kStreamThreads, 2) void fp4_stream_kernel(ColsArgs 
   wait_vm<0>();                          // zeros on their way to LDS past the last step
 }
 
+// Scale bytes of a row's 128 values from k0 on, the same in the four lanes of a
+// row: dwords of 4 scales.  One that would pass the row's end is read up to it
+// and shifted, so that nothing behind a row is touched and nothing branches.
+template <int FMT>
+struct ChunkScales {
+  static constexpr int N = FMT == 0 ? 2 : 1, SPAN = 4 * WeightFmt<FMT>::G;
+  uint32_t v[N];
+  int shift;                             // of the last dword in the row
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int k0, int K) {
+    shift = 0;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int left = K - k0 - i * SPAN;            // uniform
+      const int missing = left >= SPAN || left <= 0 ? 0 : (SPAN - left) / WeightFmt<FMT>::G;
+      const int at = (k0 + i * SPAN) / WeightFmt<FMT>::G - missing;
+      shift = missing ? 8 * missing : shift;
+      v[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(left > 0 ? row + at : kBufferEnd), 0, 0);
+    }
+  }
+  // of the values 32 q + 8 g ..
+  __device__ __forceinline__ float at(int q, int g, int left) const {
+    uint32_t w = v[FMT == 0 ? q / 2 : 0];
+    if constexpr (FMT == 0) {            // an E4M3 scale's sign bit is ignored
+      if (q < 2 ? left < 64 : left < 128) w >>= shift;         // uniform
+      w = (w & 0x7F7F7F7Fu) >> (8 * (g >> 1));
+      return q & 1 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 2) : __builtin_amdgcn_cvt_f32_fp8((int)w, 0);
+    } else {
+      return __uint_as_float((w >> (shift + 8 * q) & 0xFFu) << 23);
+    }
+  }
+};
+
+// Up to 64 tokens at a time through one matrix: the activations of a segment of
+// 512 values lie in LDS for the whole workgroup (two or three buffers, one
+// barrier a segment), the codes of two chunks of 128 values in a wave's own part.
+// A wave takes 32 rows; `wk` waves (1, 2 or 4) share rows and cut a segment's
+// chunks among them.  Eight waves: one alone on its SIMD issues half of what two
+// do.  Two more only fetch the activations: loads come back in a wave's order,
+// and one that waited for activations would wait for all codes that it asked for
+// before, from farther away.  Decoding bounds it: 48 tokens through 4096x4096
+// 16 us, by fp4_cols_kernel 23.
+constexpr int kMidWaves = 8, kMidLoaders = 2, kMidThreads = (kMidWaves + kMidLoaders) * 64;
+constexpr int kMidDepth = 2, kMidChunk = 128;
+constexpr int kMidLeast = 128;           // cols: a dword of scales in every row
+
+template <int FMT, int NT>
+__global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
+  constexpr int TOKENS = 16 * NT, KSEG = 512, BUFFERS = NT <= 2 ? 3 : 2, G = WeightFmt<FMT>::G;
+  __shared__ __attribute__((aligned(16))) uint8_t xs[BUFFERS][TOKENS * KSEG * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t cs[kMidDepth][kMidWaves][2][1024];
+  const int t = (int)threadIdx.x, lane = t & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const uint32_t slot = blockIdx.x / (uint32_t)a.row_blocks;
+  const int rb = (int)(blockIdx.x - slot * (uint32_t)a.row_blocks);
+  const int64_t first = (int64_t)slot * TOKENS;
+  const int cols = (int)(a.tokens - first < TOKENS ? a.tokens - first : TOKENS);
+  const float all = alpha_all(a.w, 0);
+  const int rows = a.w.rows, K = a.w.cols;
+  const int kpart = wave % a.wk, wr = kMidWaves / a.wk, set = wave / a.wk;
+  const int blk = rb * wr * 32, segs = (K + KSEG - 1) / KSEG;
+  const int first_seg = rb % segs;       // blocks at the same step meet on few channels
+  auto place = [&](int seg) {
+    const int p = seg + first_seg;
+    return p < segs ? p : p - segs;
+  };
+  const int rows_left = rows - blk;
+  const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(code_row<FMT>(a.w, 0, blk), (int64_t)rows_left * (K / 2));
+  const __amdgpu_buffer_rsrc_t rs =
+      buffer_rsrc(scale_row<FMT>(a.w, 0, blk),
+                  (int64_t)(a.w.tile_shift ? (rows_left + 15) / 16 : rows_left) * (K / G));
+  // direct loads of codes: lane -> row lane / 4, piece lane % 4 ^ row / 4 % 4 (16 rows'
+  // reads cover all banks); scales by the 16 lanes of the rows
+  uint32_t coff[2], soff[2];
+  const int crow = lane >> 2, cpiece = (lane & 3) ^ (crow >> 2 & 3);
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const uint32_t n = (uint32_t)(set * 32 + 16 * i);
+    coff[i] = (n + crow) * (uint32_t)(K / 2) + 16 * cpiece;
+    soff[i] = lane < 16 ? ((n + r) >> a.w.tile_shift) * (uint32_t)(K / G) : kBufferEnd;
+  }
+  struct Chunk {
+    ChunkScales<FMT> sc[2];
+    int left;                            // values to the end of a row
+  };
+  // chunks of a wave: kpart, kpart + wk, ... of every segment's four, counted through;
+  // as many loads past the end
+  const int each = 4 / a.wk;             // of a segment
+  const int rounds = (segs * each + kMidDepth - 1) / kMidDepth * kMidDepth / each;   // segments
+  auto load = [&](Chunk& f, int d, int at) {
+    const int seg = at / each;
+    const int k0 = seg < segs ? place(seg) * KSEG + (at % each * a.wk + kpart) * kMidChunk : K;
+    const int left = K - k0;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int co = (int)(32 * cpiece < left ? coff[i] + k0 / 2 : kBufferEnd);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void_t*)cs[d][wave][i], 16, co, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) f.sc[i].load(rs, soff[i], k0, K);
+    f.left = left;
+  };
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x + first * a.xs, ((cols - 1) * a.xs + K) * 2);
+  if (wave >= kMidWaves) {
+    // tokens of a loader: every second; 64 lanes take a token's segment, piece p of
+    // token c at p ^ c % 16
+    constexpr int EACH = TOKENS / kMidLoaders;
+    const int l0 = wave - kMidWaves;
+    auto fill_x = [&](int seg) {
+      const int k0 = seg < segs ? place(seg) * KSEG : K;
+      uint8_t* const buf = xs[seg % BUFFERS];
+#pragma unroll
+      for (int i = 0; i < EACH; i++) {
+        const int c = l0 + kMidLoaders * i;
+        const int k = k0 + 8 * (lane ^ (c & 15));
+        const int o = (int)((c < cols) & (k < K) ? 2 * (c * (uint32_t)a.xs + k) : kBufferEnd);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(buf + c * KSEG * 2), 16, o, 0, 0, 0);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < BUFFERS - 1; i++) fill_x(i);
+    for (int seg = 0; seg < rounds; seg++) {
+      wait_vm<(BUFFERS - 2) * EACH>();             // all but the segments after it
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      fill_x(seg + BUFFERS - 1);                   // past the end: zeros
+    }
+    wait_vm<0>();
+    __syncthreads();
+    if (a.wk > 1) __syncthreads();
+    return;
+  }
+  f32x4_t acc[2][NT] = {};
+  auto multiply = [&](const Chunk& f, int d, const uint8_t* x, int chunk) {
+    wait_vm<(2 + 2 * ChunkScales<FMT>::N) * (kMidDepth - 1)>();      // all but the later chunks
+    u32x4_t v[4][NT], cd[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      cd[i] = *(const u32x4_t*)(cs[d][wave][i] + 64 * r + 16 * (g ^ (r >> 2)));
+    ChunkScales<FMT> sc[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      sc[i].shift = f.sc[i].shift;
+#pragma unroll
+      for (int q = 0; q < ChunkScales<FMT>::N; q++)
+        sc[i].v[q] = (uint32_t)__shfl((int)f.sc[i].v[q], r, 64);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int piece = (chunk * kMidChunk + 32 * q) / 8 + g;
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+        v[q][j] = *(const u32x4_t*)(x + ((16 * j + r) * KSEG + 8 * (piece ^ r)) * 2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 2; i++) cd[i] = turn_groups(cd[i]);
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      u32x4_t op[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) op[i] = decode8<FMT>(cd[i][q], sc[i].at(q, g, f.left));
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < 2; i++) acc[i][j] = mfma16_bf16(op[i], v[q][j], acc[i][j]);
+    }
+  };
+  // straight through in rounds of kMidDepth chunks, the last ones past the end: a
+  // branch in between would have the compiler wait for all loads at once
+  Chunk f[kMidDepth];
+#pragma unroll
+  for (int d = 0; d < kMidDepth; d++) {
+    load(f[d], d, d);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int at = 0; at < rounds * each; at += kMidDepth)
+    static_for<kMidDepth>([&](auto di) {
+      constexpr int d = decltype(di)::value;
+      const int step = at + d, seg = step / each;
+      if (step % each == 0) {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
+      multiply(f[d], d, xs[seg % BUFFERS], step % each * a.wk + kpart);
+      load(f[d], d, step + kMidDepth);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  wait_vm<0>();
+  __syncthreads();                     // the last zeros have landed, and all is read
+  if (a.wk > 1) {                      // the first wave of a set takes the others' sums
+    f32x4_t(*red)[NT][2][64] = (f32x4_t(*)[NT][2][64])xs[0];
+    if (kpart)
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        red[wave][j][0][lane] = acc[0][j];
+        red[wave][j][1][lane] = acc[1][j];
+      }
+    __syncthreads();
+    if (kpart) return;
+    for (int w = 1; w < a.wk; w++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        acc[0][j] += red[wave + w][j][0][lane];
+        acc[1][j] += red[wave + w][j][1][lane];
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; j++)
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int n = blk + set * 32 + 16 * i + 4 * g, c = 16 * j + r;
+      if (c < cols && n < rows) put_rows<false>(a, 0, rows, n, first + c, all, {acc[i][j]});
+    }
+}
+
 // The down projection of a few tokens (16 and 128 assignments at most), joined
 // over their experts in the same launch: a workgroup takes 16 rows, its waves
 // the steps of all assignments in turn, each the product of one expert's rows

@@ -140,3 +140,48 @@ def test_gradients_are_refused():
         fp4.fp4_linear(handle(w), x)
     with torch.no_grad():
         fp4.fp4_linear(handle(w), x)
+
+
+@pytest.mark.parametrize("layout", ["tensor", "rows", "tiles", "mx"])
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (9, 8208, 320), (16, 9008, 1024),                                     # streams
+    (33, 7008, 544), (40, 8208, 160), (100, 4112, 1056), (150, 4112, 352),   # 32 to 64 tokens at once
+    (1030, 7024, 160), (4200, 1504, 416), (300, 20016, 96), (700, 12320, 32)])   # 128 tokens, 256 rows
+def test_large(layout, tokens, rows, cols):
+    w, x = make(tokens + rows + cols, tokens, rows, cols, layout)
+    want, err = R.linear(x, R.values(w, layout))
+    h = handle(w)
+    R.close(fp4.fp4_linear(h, x.cuda()), want, err)
+    R.close(fp4.fp4_linear(h, x.cuda(), dtype=F32), want, err)
+
+
+@pytest.mark.parametrize("layout", ["rows", "mx"])
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (13, 8193, 256), (50, 6001, 288), (70, 9001, 544), (1025, 7003, 288)])
+def test_large_odd_rows_and_strides(layout, tokens, rows, cols):
+    """Rows inside wider tensors; what lies between and behind the output's rows stays."""
+    w, x = make(tokens + rows, tokens, rows, cols, layout)
+    wide = torch.full((tokens, cols + 24), math.nan, dtype=BF)
+    wide[:, 16:16 + cols] = x
+    want, err = R.linear(x, R.values(w, layout))
+    for dtype in (BF, F32):
+        for first, width in ((0, rows), (1, rows + 4)):
+            out = torch.full((tokens + 2, width + first), 7.0, dtype=dtype, device="cuda")
+            R.close(fp4.fp4_linear(handle(w), wide.cuda()[:, 16:16 + cols], dtype=dtype,
+                                   out=out[:tokens, first:first + rows]), want, err)
+            out[:tokens, first:first + rows] = 7.0
+            assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("tokens,rows,cols", [(60, 6000, 320), (1025, 7008, 160)])
+def test_large_values_that_are_not_finite(tokens, rows, cols):
+    w, x = make(5, tokens, rows, cols, "tensor")
+    x[1, 17], x[2, 33] = math.nan, math.inf
+    got = fp4.fp4_linear(handle(w), x.cuda(), dtype=F32).cpu()
+    fine = [t for t in range(tokens) if t not in (1, 2)]
+    wv = R.values(w, "tensor")
+    R.close(got[fine], *R.linear(x[fine], wv))
+    assert got[1].isnan().all()
+    col = wv[:, 33]
+    assert (got[2][col > 0] == math.inf).all() and (got[2][col < 0] == -math.inf).all()
+    assert got[2][col == 0].isnan().all()
