@@ -14,18 +14,36 @@ constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 // expert e and those of the experts before it (every workgroup reads all ids,
 // from L2), so off[e] needs no other workgroup; then it writes its own, in
 // order, to order[off[e]] ...  Numbers outside [0, experts) are left out.
+// Latency bounds it, so a wave asks for kPlanAhead runs of ids at once (24576
+// assignments of 64 experts: one run at a time 17.0 us, 8 9.3).
+constexpr int kPlanAhead = 8;
+
 __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t* __restrict__ ids,
                                                                    int n, int experts,
-                                                                   int32_t* off, int32_t* order) {
+                                                                   int32_t* __restrict__ off,
+                                                                   int32_t* __restrict__ order) {
   __shared__ int mine_of[kPlanWaves], less_of[kPlanWaves];
-  const int e = (int)blockIdx.x, t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int e = (int)blockIdx.x, t = (int)threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t per = ((int64_t)n + kPlanThreads - 1) / kPlanThreads * 64;   // ids of a wave
   const int64_t i0 = wave * per, i1 = i0 + per < n ? i0 + per : n;
+  auto runs = [&](int64_t i, int (&id)[kPlanAhead]) {
+#pragma unroll
+    for (int r = 0; r < kPlanAhead; r++) {
+      const int64_t at = i + 64 * r + lane;
+      id[r] = ids[at < n ? at : n - 1];
+      if (at >= i1) id[r] = -1;
+    }
+  };
   int mine = 0, less = 0;                // of the wave
-  for (int64_t i = i0; i < i1; i += 64) {
-    const int id = i + lane < i1 ? ids[i + lane] : -1;
-    mine += __popcll(__ballot(id == e));
-    less += __popcll(__ballot(id >= 0 && id < e));
+  for (int64_t i = i0; i < i1; i += 64 * kPlanAhead) {
+    int id[kPlanAhead];
+    runs(i, id);
+#pragma unroll
+    for (int r = 0; r < kPlanAhead; r++) {
+      mine += __popcll(__ballot(id[r] == e));
+      less += __popcll(__ballot(id[r] >= 0 && id[r] < e));
+    }
   }
   if (lane == 0) {
     mine_of[wave] = mine;
@@ -43,11 +61,15 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
     off[experts] = total;
   }
   if (!mine) return;
-  for (int64_t i = i0; i < i1; i += 64) {
-    const bool here = i + lane < i1 && ids[i + lane] == e;
-    const uint64_t m = __ballot(here);
-    if (here) order[at + __popcll(m & ((1ull << lane) - 1))] = (int32_t)(i + lane);
-    at += __popcll(m);
+  for (int64_t i = i0; i < i1; i += 64 * kPlanAhead) {
+    int id[kPlanAhead];
+    runs(i, id);
+#pragma unroll
+    for (int r = 0; r < kPlanAhead; r++) {
+      const uint64_t m = __ballot(id[r] == e);
+      if (id[r] == e) order[at + __popcll(m & ((1ull << lane) - 1))] = (int32_t)(i + 64 * r + lane);
+      at += __popcll(m);
+    }
   }
 }
 

@@ -178,7 +178,7 @@ inline bool tall(int64_t rows, int64_t slots) {
 }
 
 // A round of 128x256 tiles takes as long as six and a half of 64 tokens x 64 rows
-// (88 us and 13.5 with 4096 columns, whose tiles decode their weights for twice
+// (88 us and 14 with 4096 columns, whose tiles decode their weights for twice
 // the tokens but wait for each other): whichever has done sooner.
 inline bool tiles_sooner(int64_t tokens, int64_t rows) {
   const int64_t tiles = cdiv(tokens, kTileTokens) * cdiv(rows, kTileWeights);
