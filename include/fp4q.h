@@ -438,7 +438,8 @@ size_t fp4_linear_workspace_bytes(const fp4_weights* w, int64_t tokens);
 /* out[t][n] = sum_k x[t][k] w[n][k] for one matrix (experts 1).  The products
  * of x with q * Delta (or q * 2^k) are exact, their sums fp32, and alpha is
  * applied to the sum.  out is bf16, or fp32 with out_f32, aligned to its
- * elements, out_stride any number from rows on.  Equal calls give equal bits. */
+ * elements, out_stride any number from rows on.  out may not overlap x.  Equal
+ * calls give equal bits. */
 int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_t tokens,
                void* out, int64_t out_stride, int out_f32, void* ws, size_t ws_bytes, void* stream);
 
