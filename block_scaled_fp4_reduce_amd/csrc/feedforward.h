@@ -171,8 +171,17 @@ inline int linear_tiles(int64_t tokens, int64_t rows) {
   return 4;
 }
 
+// Streams for matrices of many rows, the more the more tokens: a workgroup waits for
+// all of its activations first (4096 columns of NVFP4, streams and cols: 1 token of
+// 4096 rows 8.6 and 7.6 us, 8192 8.7 and 9.2, 28672 19.4 and 24.5; 8 tokens 8192 12.6
+// and 9.7, 14336 13.9 and 15.5; 16 tokens 14336 23.3 and 17.8, 28672 24.3 and 31.5).
+inline bool streams_sooner(const fp4_weights* w, int64_t tokens) {
+  return w->rows >= 8192 && w->rows >= 1792 * tokens && stream_fits(w);
+}
+
 // Two row tiles a wave, so that a token's activations are read for 32 rows at a
-// time, where that leaves work for three CUs of four.
+// time, where that leaves work for three CUs of four (16 tokens through 14336x4096
+// 17.8 us, one tile 24.4; through 4096x4096 10.8 and 8.6).
 inline bool tall(int64_t rows, int64_t slots) {
   return cdiv(rows, 32) * slots * 4 >= 3 * (int64_t)num_cus();
 }
@@ -191,6 +200,19 @@ inline bool tiles_sooner(int64_t tokens, int64_t rows) {
 // go in slices of tokens, one after another in the same workspace.
 constexpr int64_t kSliceBytes = 0x7FFF0000;
 
+// More tokens an expert than streams, 16 at a time, are worth (64 and 128 experts,
+// NVFP4: 16 tokens each 186 us by streams, 257 by tiles, and 441, 492; 24 246, 260
+// and 583, 500; MXFP4: 24 195, 246 and 439, 501; 32 243, 250 and 525, 525).
+inline bool crowded(const fp4_weights* gu, int64_t n) {
+  return n > (gu->format == FP4_FORMAT_NVFP4 ? 20 : 32) * gu->experts;
+}
+
+// Few enough assignments that the down projection joins them itself (32: 49 us
+// with 64 experts and 62 with 128, by streams and a join 48 and 69; 96: 138 and 79).
+inline bool few(const fp4_weights* dn, int64_t tokens, int64_t n) {
+  return tokens <= 16 && n <= kFewMost && stream_fits(dn);
+}
+
 struct ExpertsPlan {
   int64_t tokens;                        // of a slice
   int64_t n;                             // its assignments
@@ -204,7 +226,7 @@ inline ExpertsPlan experts_plan(const fp4_weights* gu, const fp4_weights* dn, in
   const int64_t most = kSliceBytes / (2 * top_k * dn->cols);
   p.tokens = tokens < most ? tokens : most;
   p.n = p.tokens * top_k;
-  p.inline_rows = p.n <= kInlineMost;
+  p.inline_rows = p.n <= kInlineMost && (!crowded(gu, p.n) || few(dn, p.tokens, p.n));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -269,7 +291,7 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
   if (!p.inline_rows)
     err = launch(expert_plan_kernel, (unsigned)e, kPlanThreads, st, experts, (int)n, e,
                  (int32_t*)(ws + p.off), (int32_t*)(ws + p.order));
-  if (tokens <= 16 && n <= kFewMost && stream_fits(down)) {
+  if (p.inline_rows && few(down, tokens, n)) {
     if (stream_fits(gate_up))
       err = launch_stream<true, kInline>(gate_up->format, a, slots, slots < e ? slots : e, tokens, st);
     else
@@ -291,7 +313,7 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
                          ? launch_stream<false, S>(down->format, b, slots, busy, tokens, st)
                          : launch_cols<2, false, S>(down->format, b, slots, st));
   };
-  if (!p.inline_rows && n > 32 * (int64_t)e) {
+  if (!p.inline_rows && crowded(gate_up, n)) {
     TiledArgs ta = tiled_args(a), tb = tiled_args(b);
     ta.tiles_t = tb.tiles_t = (uint32_t)(n / kTileTokens + e);
     ta.out_vec = tb.out_vec = 1;
@@ -470,7 +492,7 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
     t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
     return launched(launch_tiled<false, false>(w->format, t, st));
   }
-  if (tokens <= 16 && w->rows >= 8192 && stream_fits(w))
+  if (tokens <= 16 && streams_sooner(w, tokens))
     return launched(launch_stream<false, kDense>(w->format, a, 1, 1, tokens, st));
   if (tokens <= 16 || w->cols < kMidLeast) {
     const int64_t slots = cdiv(tokens, 16);

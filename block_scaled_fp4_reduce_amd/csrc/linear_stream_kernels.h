@@ -388,7 +388,8 @@ __global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
       for (int i = 0; i < EACH; i++) {
         const int c = l0 + kMidLoaders * i;
         const int k = k0 + 8 * (lane ^ (c & 15));
-        const int o = (int)((c < cols) & (k < K) ? 2 * (c * (uint32_t)a.xs + k) : kBufferEnd);
+        const bool in = (c < cols) & (k < K);
+        const int o = (int)(in ? 2 * (c * (uint32_t)a.xs + k) : kBufferEnd);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(buf + c * KSEG * 2), 16, o, 0, 0, 0);
       }
     };
@@ -489,13 +490,13 @@ __global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
     }
 }
 
-// The down projection of a few tokens (16 and 128 assignments at most), joined
+// The down projection of a few tokens (16 and 32 assignments at most), joined
 // over their experts in the same launch: a workgroup takes 16 rows, its waves
 // the steps of all assignments in turn, each the product of one expert's rows
 // with one hidden row, which lands in its token's column of the sum with its
 // weight.  An expert of several tokens is decoded for each of them.  Latency
 // bounds it: 1 token, 6 experts of 1408 x 2048 8.4 us.
-constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kFewMost = 128;
+constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kFewMost = 32;
 
 struct FewStep {
   uint8_t code[2048], scale[256], x[1024];
@@ -510,17 +511,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void fp4_down_few_kernel(ColsArgs a
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int n = (int)(a.tokens * a.top_k), K = a.w.cols, rows = a.w.rows, blk = (int)blockIdx.x * 16;
   const int steps = (K + kColsStep - 1) / kColsStep, units = n * steps;
-  // assignments lane and lane + 64
-  int id[2];
-  float wt[2];
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int at = lane + 64 * i;
-    id[i] = at < n ? a.ids[at] : -1;
-    wt[i] = at < n ? weights[at] : 0.0f;
-    if (id[i] < 0 || id[i] >= a.experts) id[i] = -1;
-  }
-  auto expert = [&](int at) { return __builtin_amdgcn_readlane(at < 64 ? id[0] : id[1], at & 63); };
+  int id = lane < n ? a.ids[lane] : -1;              // of assignment `lane`
+  const float wt = lane < n ? weights[lane] : 0.0f;
+  if (id < 0 || id >= a.experts) id = -1;
+  auto expert = [&](int at) { return __builtin_amdgcn_readlane(id, at); };
   const int crow = lane >> 3, cpiece = lane & 7, srow = lane / SD, sdw = lane % SD;
   const int left = rows - blk;
   const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, a.x_bytes);
@@ -578,8 +572,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void fp4_down_few_kernel(ColsArgs a
       for (int q = 0; q < 4; q++)
         acc = mfma16_bf16(decode8<FMT>(cd[q], sc.at(h, q, g)), x[4 * h + q], acc);
     }
-    const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
-        (int)__float_as_uint(at < 64 ? wt[0] : wt[1]), at & 63));
+    const float w =
+        __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(wt), at));
     if (r == at / a.top_k) {             // every column holds the product: its token's takes it
       const float all = alpha_all(a.w, e);
 #pragma unroll

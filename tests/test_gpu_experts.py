@@ -125,3 +125,12 @@ def test_gradients_are_refused():
         b[i] = a[i].clone().requires_grad_()
         with pytest.raises(RuntimeError, match="no backward"):
             fp4.fp4_experts(*b)
+
+
+@pytest.mark.parametrize("layout", ["rows", "mx"])
+@pytest.mark.parametrize("tokens,experts,k", [
+    (16, 1, 1), (10, 1, 1), (16, 2, 2), (4, 20, 8), (5, 20, 8), (11, 3, 3), (60, 8, 2), (80, 8, 2),
+    (81, 8, 2), (128, 8, 2), (129, 8, 2), (64, 2, 2), (256, 12, 2), (257, 12, 2)])
+def test_sizes_next_to_each_other(layout, tokens, experts, k):
+    """Around the numbers of assignments at which another kernel takes the call."""
+    check(*make(tokens + experts, tokens, experts, k, 256, 128, layout), layout)

@@ -185,3 +185,13 @@ def test_large_values_that_are_not_finite(tokens, rows, cols):
     col = wv[:, 33]
     assert (got[2][col > 0] == math.inf).all() and (got[2][col < 0] == -math.inf).all()
     assert got[2][col == 0].isnan().all()
+
+
+@pytest.mark.parametrize("layout", ["tensor", "tiles", "mx"])
+@pytest.mark.parametrize("tokens,rows", [(4, 8176), (4, 8192), (5, 8960), (5, 8944), (16, 28672), (17, 4096),
+                                         (64, 4112), (65, 4112), (16, 6144)])
+def test_sizes_next_to_each_other(layout, tokens, rows):
+    """Around the sizes at which another kernel takes the call."""
+    w, x = make(tokens + rows, tokens, rows, 256, layout)
+    want, err = R.linear(x, R.values(w, layout))
+    R.close(fp4.fp4_linear(handle(w), x.cuda()), want, err)
