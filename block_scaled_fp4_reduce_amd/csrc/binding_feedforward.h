@@ -19,7 +19,7 @@ Rows rows_of(const at::Tensor& x, at::ScalarType type, int64_t rows, int64_t col
   Rows r{x.data_ptr(), x.size(1), x.size(0), x.size(1)};
   if (r.rows && r.cols > 1 && x.stride(1) != 1)
     fail(PyExc_ValueError, std::string(what) + ": the values of a row must be contiguous");
-  if (r.rows > 1) r.stride = x.stride(0);
+  if (r.rows > 1 && r.cols > 0) r.stride = x.stride(0);
   return r;
 }
 

@@ -176,7 +176,7 @@ inline int linear_tiles(int64_t tokens, int64_t rows) {
 // 4096 rows 8.6 and 7.6 us, 8192 8.7 and 9.2, 28672 19.4 and 24.5; 8 tokens 8192 12.6
 // and 9.7, 14336 13.9 and 15.5; 16 tokens 14336 23.3 and 17.8, 28672 24.3 and 31.5).
 inline bool streams_sooner(const fp4_weights* w, int64_t tokens) {
-  return w->rows >= 8192 && w->rows >= 1792 * tokens && stream_fits(w);
+  return w->rows >= 8192 && w->rows >= 1792 * tokens && w->cols > 0 && stream_fits(w);
 }
 
 // Two row tiles a wave, so that a token's activations are read for 32 rows at a

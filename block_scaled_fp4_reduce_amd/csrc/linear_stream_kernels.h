@@ -300,7 +300,8 @@ struct ChunkScales {
       w = (w & 0x7F7F7F7Fu) >> (8 * (g >> 1));
       return q & 1 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 2) : __builtin_amdgcn_cvt_f32_fp8((int)w, 0);
     } else {
-      return __uint_as_float((w >> (shift + 8 * q) & 0xFFu) << 23);
+      // past the row's end any of its scales: the codes there are zeros
+      return __uint_as_float((w >> ((shift + 8 * q) & 31) & 0xFFu) << 23);
     }
   }
 };
@@ -313,7 +314,7 @@ struct ChunkScales {
 // do.  Two more only fetch the activations: loads come back in a wave's order,
 // and one that waited for activations would wait for all codes that it asked for
 // before, from farther away.  Decoding and its waits bound it: 48 tokens through
-// 14336x4096 of MXFP4 14.2 us (codes, activations and outputs at the rate of a
+// 14336x4096 of MXFP4 15.0 us (codes, activations and outputs at the rate of a
 // copy: 6.7), by fp4_cols_kernel 23.
 constexpr int kMidWaves = 8, kMidLoaders = 2, kMidThreads = (kMidWaves + kMidLoaders) * 64;
 constexpr int kMidDepth = 2, kMidChunk = 128;
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
     return;
   }
   f32x4_t acc[2][NT] = {};
-  auto multiply = [&](const Chunk& f, int d, const uint8_t* x, int chunk) {
+  auto multiply = [&](Chunk& f, int d, const uint8_t* x, int chunk, int next) {
     wait_vm<(2 + 2 * ChunkScales<FMT>::N) * (kMidDepth - 1)>();      // all but the later chunks
     u32x4_t v[4][NT], cd[2];
 #pragma unroll
@@ -431,11 +432,15 @@ __global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 2; i++) cd[i] = turn_groups(cd[i]);
+    const int left = f.left;
+    __builtin_amdgcn_sched_barrier(0);   // the codes are in registers: their buffer is free
+    load(f, d, next);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < 4; q++) {
       u32x4_t op[2];
 #pragma unroll
-      for (int i = 0; i < 2; i++) op[i] = decode8<FMT>(cd[i][q], sc[i].at(q, g, f.left));
+      for (int i = 0; i < 2; i++) op[i] = decode8<FMT>(cd[i][q], sc[i].at(q, g, left));
 #pragma unroll
       for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -458,8 +463,7 @@ __global__ __launch_bounds__(kMidThreads, 3) void fp4_mid_kernel(ColsArgs a) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
       }
-      multiply(f[d], d, xs[seg % BUFFERS], step % each * a.wk + kpart);
-      load(f[d], d, step + kMidDepth);
+      multiply(f[d], d, xs[seg % BUFFERS], step % each * a.wk + kpart, step + kMidDepth);
       __builtin_amdgcn_sched_barrier(0);
     });
   wait_vm<0>();

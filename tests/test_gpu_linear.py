@@ -195,3 +195,25 @@ def test_sizes_next_to_each_other(layout, tokens, rows):
     w, x = make(tokens + rows, tokens, rows, 256, layout)
     want, err = R.linear(x, R.values(w, layout))
     R.close(fp4.fp4_linear(handle(w), x.cuda()), want, err)
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 300])
+@pytest.mark.parametrize("rows", [48, 9008])
+def test_no_columns(tokens, rows):
+    """Empty sums are zeros."""
+    empty = lambda: torch.empty(rows, 0, dtype=torch.uint8, device="cuda")
+    out = torch.full((tokens, rows), 7.0, dtype=BF, device="cuda")
+    h = fp4.Fp4Weights(empty(), empty(), torch.ones(1, device="cuda"))
+    fp4.fp4_linear(h, torch.empty(tokens, 0, dtype=BF, device="cuda"), out=out)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("layout", ["rows", "mx"])
+@pytest.mark.parametrize("cols", [128, 160, 192, 224, 256, 480, 512, 544, 608, 1024, 1056])
+@pytest.mark.parametrize("tokens", [17, 40, 64])
+def test_ends_of_rows(layout, cols, tokens):
+    """Rows that end anywhere within a run of values, and whose neighbours' scales are far larger."""
+    w, x = make(cols + tokens, tokens, 6000, cols, layout)
+    w["scales"][1::2] = 0x7E if layout == "rows" else 180
+    want, err = R.linear(x, R.values(w, layout))
+    R.close(fp4.fp4_linear(handle(w), x.cuda(), dtype=F32), want, err)
