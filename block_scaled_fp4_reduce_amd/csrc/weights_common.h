@@ -35,7 +35,6 @@ constexpr uint32_t kBufferEnd = 0x7FFFFF00u;
 template <int FMT>
 struct WeightFmt {
   static constexpr int G = FMT == 0 ? 16 : 32;
-  static constexpr int PER32 = 32 / G;   // scales of 32 codes
 };
 
 // Row n of expert e.
@@ -54,25 +53,6 @@ __device__ __forceinline__ float alpha_all(const WeightView& w, int64_t e) {
 // A row's factor, all = alpha_all.
 __device__ __forceinline__ float alpha_row(const WeightView& w, int64_t e, int n, float all) {
   return w.row_alpha ? w.alpha[e * w.alpha_e + n] : all;
-}
-
-// The scale bytes of the 32 codes from k on (k a multiple of 32).
-template <int FMT>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int k) {
-  if constexpr (FMT == 0) return *(const uint16_t*)(row + k / 16);
-  else return row[k / 32];
-}
-
-// Scales of the two halves of 32 codes, as the decode takes them.
-template <int FMT>
-__device__ __forceinline__ void scale_values(uint32_t bytes, float (&s)[2]) {
-  if constexpr (FMT == 0) {              // an E4M3 scale's sign bit is ignored
-    const float2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)(bytes & 0x7F7Fu), 1.0f, false);
-    s[0] = v[0];
-    s[1] = v[1];
-  } else {
-    s[0] = s[1] = __uint_as_float(bytes << 23);
-  }
 }
 
 // Eight codes (even element low) to a bf16 operand.
