@@ -90,7 +90,8 @@ inline bool stream_fits(const fp4_weights* w) {
 }
 
 // busy: workgroups' worth of experts that can have tokens; tokens: an upper bound
-// of an expert's.  Where rows are few their K is cut until every CU has a
+// of an expert's where no token names it twice, for which a segment is sized.
+// Where rows are few their K is cut until every CU has a
 // workgroup.  Where they are many a workgroup takes several blocks, up to four
 // rounds of workgroups, since experts have unequal numbers of tokens (64 tokens
 // through 128 experts, gate and up: 1 round 161 us, 2 131, 4 120, 8 120).
@@ -98,12 +99,11 @@ template <bool GATED, int SRC>
 hipError_t launch_stream(int format, ColsArgs a, int64_t slots, int64_t busy, int64_t tokens,
                          hipStream_t st) {
   const int64_t rows = GATED ? a.inner : a.w.rows, wave_rows = GATED ? 16 : 32;
-  int shift = 9;                         // of a segment: as much as fits, at most all of K
-  const int64_t cols = tokens < 16 ? tokens : 16;
-  while ((cols << (shift + 2)) <= kStreamX && (1 << shift) < a.w.cols) shift++;
-  a.kseg_shift = shift;
+  const StreamSegment seg = stream_segment(tokens, a.w.cols);
+  a.kseg_shift = seg.shift;
+  a.span = seg.span;
   a.wk = 1;
-  while (a.wk < kStreamWaves && 1024 * a.wk <= (1 << shift) && 512 * a.wk < a.w.cols &&
+  while (a.wk < kStreamWaves && 1024 * a.wk <= (1 << seg.shift) && 512 * a.wk < a.w.cols &&
          cdiv(rows, wave_rows * (kStreamWaves / a.wk)) * busy < num_cus())
     a.wk *= 2;
   const int64_t all = cdiv(rows, wave_rows * (kStreamWaves / a.wk));

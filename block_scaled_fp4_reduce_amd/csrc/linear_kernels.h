@@ -38,7 +38,7 @@ struct ColsArgs {
   int top_k, experts;
   int inner;                             // gated: F
   int wk;                                // waves that share a row's K
-  int kseg_shift, blocks;                // streams: log2 of a segment of K, row blocks
+  int kseg_shift, span, blocks;          // streams: log2 of a segment of K, columns at a time, row blocks
   int row_blocks;                        // of a matrix (or of F)
   int out_f32, out_vec;                  // fp32 outputs; 4 of them may be stored at once
   int x_per_token;                       // experts: rows of x are tokens (else assignments)

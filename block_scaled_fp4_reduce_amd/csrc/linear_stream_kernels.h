@@ -29,6 +29,30 @@ namespace fp4q {
 
 constexpr int kStreamWaves = 4, kStreamThreads = kStreamWaves * 64;
 constexpr int kStreamX = 16384;          // bytes of a segment of activations
+constexpr int kStreamLeast = 9;          // log2 of the least segment, of which 16 columns fit
+
+// A segment of K: as much as fits for `tokens` columns (16 at a time), at most all
+// of it, and the columns that are taken at once, as many as fit.  An expert that a
+// token names twice has more columns than there are tokens: they take more turns.
+struct StreamSegment {
+  int shift, span;
+};
+constexpr StreamSegment stream_segment(int64_t tokens, int cols) {
+  const int64_t most = tokens < 16 ? tokens : 16;
+  int shift = kStreamLeast;
+  while ((most << (shift + 2)) <= kStreamX && (1 << shift) < cols) shift++;
+  const int fit = kStreamX >> (shift + 1);
+  return {shift, fit < 16 ? fit : 16};
+}
+constexpr bool stream_segments_fit() {
+  for (int64_t tokens = 1; tokens <= 17; tokens++)
+    for (int cols = 32; cols < 1 << 22; cols *= 2) {
+      const StreamSegment s = stream_segment(tokens, cols + 32);
+      if ((int64_t)s.span << (s.shift + 1) > kStreamX || s.span < (tokens < 16 ? tokens : 16)) return false;
+    }
+  return true;
+}
+static_assert(stream_segments_fit(), "the columns of a turn stay in their buffer");
 
 // One step of a wave in LDS: [tile][row][128 bytes of codes], 16-byte piece p of
 // row r at p ^ (r / 2 % 8), so that 16 rows' reads cover all banks; scales
@@ -137,8 +161,8 @@ __global__ __launch_bounds__(kStreamThreads, 2) void fp4_stream_kernel(ColsArgs 
       SRC == kDense ? buffer_rsrc(a.x + first * a.xs, ((count - 1) * a.xs + K) * 2)
                     : buffer_rsrc(a.x, a.x_bytes);
 
-  for (int64_t c0 = 0; c0 < count; c0 += 16) {
-    const int cols = (int)(count - c0 < 16 ? count - c0 : 16);
+  for (int64_t c0 = 0; c0 < count; c0 += a.span) {
+    const int cols = (int)(count - c0 < a.span ? count - c0 : a.span);
     // a wave's rows of x: wave, wave + 4, ...; 64 lanes take 512 values at once,
     // piece p of row c at p ^ c % 16
     uint32_t xoff[4];
