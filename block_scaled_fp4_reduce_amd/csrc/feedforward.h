@@ -284,7 +284,9 @@ inline hipError_t experts_slice(const fp4_weights* gate_up, const fp4_weights* d
   b.x_per_token = 0;
   a.x_bytes = ((tokens - 1) * x_stride + gate_up->cols) * 2;
   b.x_bytes = n * inner * 2;
-  const int64_t slots = p.inline_rows && n < e ? n : e;
+  // workgroups' experts: those that have assignments (inline_expert), of one token its
+  // assignments themselves, of which there may be more than experts
+  const int64_t slots = p.inline_rows && (n < e || tokens == 1) ? n : e;
   const int64_t quads = tokens * (down->rows / 4);
   if (cdiv(quads, kJoinThreads) >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
   hipError_t err = hipSuccess;

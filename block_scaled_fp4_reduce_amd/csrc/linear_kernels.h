@@ -51,7 +51,8 @@ enum { kDense = 0, kPlanned = 1, kInline = 2 };
 // The slot-th of the experts that have assignments, by number: workgroups ask for
 // it by themselves, without a launch before, and their list has no holes
 // (hardware deals workgroups out to the XCDs in turn, and holes unbalance
-// them).  -1 if there are fewer.  One token: the slot-th assignment's expert.
+// them).  -1 if there are fewer.  One token: the slot-th assignment's expert,
+// so that there are as many slots as assignments.
 template <int W>
 __device__ __forceinline__ int inline_expert(const ColsArgs& a, int slot) {
   if (a.tokens == 1) {

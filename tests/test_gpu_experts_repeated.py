@@ -44,3 +44,16 @@ def test_many_places(tokens, k, hidden, inner):
     g = torch.Generator().manual_seed(k)
     w = torch.softmax(torch.randn(tokens, k, generator=g), 1)
     check(gu, dn, x, w, torch.randint(-1, 5, (tokens, k), generator=g).int() * 9, "tensor")
+
+
+@pytest.mark.parametrize("layout", ["rows", "mx"])
+@pytest.mark.parametrize("hidden,inner", [(96, 160), (256, 128), (128, 96), (4096, 128)])
+@pytest.mark.parametrize("experts,k", [(1, 2), (1, 64), (3, 4), (4, 5), (4, 6), (4, 33), (20, 64)])
+def test_more_places_than_experts(layout, hidden, inner, experts, k):
+    """One token: experts that come late among its places, behind repeated ones and none."""
+    gu, dn, x, w, ids = make(k + hidden, 1, experts, 1, hidden, inner, layout)
+    w = torch.softmax(torch.randn(1, k, generator=torch.Generator().manual_seed(k)), 1)
+    late = torch.arange(k, dtype=torch.int32)[None] - (k - experts)      # each once, at the end
+    check(gu, dn, x, w, late.clamp(min=-1), layout)
+    check(gu, dn, x, w, late.clamp(min=0), layout)
+    check(gu, dn, x, w, late % experts, layout)
