@@ -17,6 +17,11 @@
 // bits; where one more might belong to them, or the groups' sizes are too close
 // for fp32 (about one token in 10^4), the wave does the token again in 64 bits.
 //
+// Renormalized weights are quotients of the chosen scores, formed from
+// scores over a power of e that the chosen have in common (choice_top), since the
+// scores themselves may lie below fp32: sigmoids of logits below -88, and with a
+// bias softmax's of logits that far below the largest.
+//
 // 16384 tokens of 256 experts, sigmoid, bias, 4 of 8 groups, 8 chosen: 17.0 us
 // forward and 11.5 backward; forward by a wave a token 28.7, all in 64 bits 48.8.
 #pragma once
@@ -108,6 +113,25 @@ __device__ __forceinline__ int best_lane(uint64_t key) {
   return __builtin_ctzll(m);
 }
 
+// A chosen score over e^m, with m the largest choice_top(l) of a token's chosen: of
+// softmax e^(l - m), of sigmoid e^(min(l, 0) - m) / (1 + e^-|l|).  Sigmoids that
+// are all below e^kLeastSigmoid, the range of 64 bits, count as 0.
+constexpr float kLeastSigmoid = -708.0f;
+template <typename T>
+__device__ __forceinline__ T choice_top(T l, int sigmoid) {
+  return sigmoid && l > (T)0 ? (T)0 : l;
+}
+__device__ __forceinline__ float choice_score(float l, float m, int sigmoid) {
+  if (!sigmoid) return expf(l - m);
+  if (m < kLeastSigmoid) return 0.0f;
+  return expf(choice_top(l, 1) - m) / (1.0f + expf(-fabsf(l)));
+}
+__device__ __forceinline__ double choice_score(double l, double m, int sigmoid) {
+  if (!sigmoid) return exp(l - m);
+  if (m < (double)kLeastSigmoid) return 0.0;
+  return exp(choice_top(l, 1) - m) / (1.0 + exp(-fabs(l)));
+}
+
 // A lane's value in every lane.
 __device__ __forceinline__ float from_lane(float v, int l) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
@@ -120,11 +144,10 @@ __device__ __forceinline__ double from_lane(double v, int l) {
 }
 
 // A token by the whole wave in 64 bits, whatever its groups: lane l holds its
-// experts from V l on.  Lane j gets the j-th expert and its score (-1 and 0 if
-// there is none), every lane the sum of the chosen scores.
+// experts from V l on.  Lane j gets the j-th expert and its weight but for the scale
+// (-1 and 0 if there is none).
 template <int V, bool BF16>
-__device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double& mine_s, int& mine_e,
-                                         double& sum) {
+__device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double& mine_s, int& mine_e) {
   const int lane = (int)threadIdx.x & 63;
   float x[V], bias[V];
   load_lane<V, BF16>(a.logits, tok * a.stride, a.experts, -INFINITY, x);
@@ -132,6 +155,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
   for (int v = 0; v < V; v++) bias[v] = 0.0f;
   if (a.bias) load_lane<V, false>(a.bias, 0, a.experts, 0.0f, bias);
   double s[V], c[V];
+  double t = 0.0;                        // softmax's sum
   if (a.sigmoid) {
 #pragma unroll
     for (int v = 0; v < V; v++) s[v] = 1.0 / (1.0 + exp(-(double)x[v]));
@@ -142,7 +166,6 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
     const double top = m == -INFINITY ? 0.0 : (double)m;
-    double t = 0.0;
 #pragma unroll
     for (int v = 0; v < V; v++) {
       s[v] = exp((double)x[v] - top);
@@ -233,7 +256,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
       if (!((kept >> ((lane * V + v) / per & 63)) & 1)) key[v] = 0;
     }
   }
-  mine_s = sum = 0.0;
+  mine_s = 0.0;
   mine_e = -1;
   for (int j = 0; j < a.top_k; j++) {
     uint64_t best = key[0];
@@ -250,7 +273,6 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
     if (l < 0) break;
     const double won = from_lane(bs, l);
     const int e = l * V + __builtin_amdgcn_readlane(at, l);
-    sum += won;
     if (lane == j) {
       mine_s = won;
       mine_e = e;
@@ -258,6 +280,15 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
 #pragma unroll
     for (int v = 0; v < V; v++) key[v] = lane == l && at == v ? 0 : key[v];
   }
+  if (!a.renormalize) return;
+  const double l = mine_e < 0 ? -INFINITY : (double)logit_at<BF16>(a.logits, tok * a.stride + mine_e);
+  double m = choice_top(l, a.sigmoid);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));
+  mine_s = mine_e < 0 ? 0.0 : choice_score(l, m, a.sigmoid);
+  if (mine_e >= 0 && t != t) mine_s = t;             // the whole token's NaN
+  const double sum = wave_total(mine_s);
+  mine_s = sum == 0.0 ? 0.0 : mine_s / sum;
 }
 
 // Reductions over the LPT lanes of a token; every lane gets the result.
@@ -445,7 +476,12 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   }
   const bool in = chosen >= 0 && place < a.top_k;
   float s = 0.0f;
-  if (in) s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / total;
+  if (a.renormalize) {
+    const float m = token_max<LPT>(in ? choice_top(l, a.sigmoid) : -INFINITY);
+    if (in) s = choice_score(l, m, a.sigmoid);
+  } else if (in) {
+    s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / total;
+  }
   if (!a.sigmoid && a.renormalize) {
     // the whole token's NaN and infinities, which its sum would carry
     bool bad = false;
@@ -473,11 +509,10 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   for (int i = 0; i < TOKENS; i++) {
     const uint64_t own = LPT == 64 ? ~0ull : 0xFFFFull << (16 * i);
     if (!(again & own) || first + i >= a.tokens) continue;
-    double s64, sum64;
+    double s64;
     int e;
-    choose64<(LPT * V + 63) / 64, BF16>(a, first + i, s64, e, sum64);
+    choose64<(LPT * V + 63) / 64, BF16>(a, first + i, s64, e);
     if (lane < a.top_k) {
-      if (a.renormalize) s64 = sum64 == 0.0 ? 0.0 : s64 / sum64;
       weights[(first + i) * a.top_k + lane] = e < 0 ? 0.0f : (float)((double)a.scale * s64);
       experts[(first + i) * a.top_k + lane] = e;
     }
@@ -491,11 +526,10 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route64_kernel(RouteArgs
   const int lane = (int)threadIdx.x & 63;
   const int64_t tok = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
   if (tok >= a.tokens) return;
-  double s, sum;
+  double s;
   int e;
-  choose64<V, BF16>(a, tok, s, e, sum);
+  choose64<V, BF16>(a, tok, s, e);
   if (lane < a.top_k) {
-    if (a.renormalize) s = sum == 0.0 ? 0.0 : s / sum;
     weights[tok * a.top_k + lane] = e < 0 ? 0.0f : (float)((double)a.scale * s);
     experts[tok * a.top_k + lane] = e;
   }
@@ -520,21 +554,15 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_backward_kernel(
 #pragma unroll
   for (int v = 0; v < V; v++) out[v] = 0.0f;
   float d;                               // what lands on the lane's chosen expert
-  if (a.sigmoid) {
-    const float s = there ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-    const float not_s = 1.0f / (1.0f + expf(l));
-    if (a.renormalize) {
-      const float sum = token_sum<LPT>(s), p = sum == 0.0f ? 0.0f : s / sum;
-      d = p * not_s * (g - token_sum<LPT>(p * g));
-    } else {
-      d = s * not_s * g;
-    }
-  } else if (a.renormalize) {
-    const float m = token_max<LPT>(l);
-    float p = there ? expf(l - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+  if (a.renormalize) {
+    const float m = token_max<LPT>(choice_top(l, a.sigmoid));
+    float p = there ? choice_score(l, m == -INFINITY && !a.sigmoid ? 0.0f : m, a.sigmoid) : 0.0f;
     const float sum = token_sum<LPT>(p);
     p = sum == 0.0f ? 0.0f : p / sum;
     d = p * (g - token_sum<LPT>(p * g));
+    if (a.sigmoid) d *= 1.0f / (1.0f + expf(l));
+  } else if (a.sigmoid) {
+    d = there ? 1.0f / (1.0f + expf(-l)) * (1.0f / (1.0f + expf(l))) * g : 0.0f;
   } else {
     float x[V];
     const int64_t at = tok * a.stride + e0;

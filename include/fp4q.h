@@ -452,7 +452,9 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
  * group_top 2 the sum of its two largest s (+ bias) among candidates.  The top_k
  * candidates of largest c follow in that order (ties, of groups also: the lower
  * index first), each with
- *   weight = scale s_i, or with renormalize  scale s_i / sum of the chosen s.
+ *   weight = scale s_i, or with renormalize  scale s_i / sum of the chosen s
+ * (a quotient in the range of fp32 where the scores leave it; sigmoids of
+ * logits that are all below -708 give weights 0).
  * Places without a candidate get expert -1 and weight 0.  A NaN or +inf among
  * softmax's logits makes the weights of its chosen experts NaN. */
 typedef struct {
