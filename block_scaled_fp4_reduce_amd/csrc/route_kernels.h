@@ -132,6 +132,13 @@ __device__ __forceinline__ double choice_score(double l, double m, int sigmoid) 
   return exp(choice_top(l, 1) - m) / (1.0 + exp(-fabs(l)));
 }
 
+// A score as a term of its group's size: where softmax's are NaN, all of them
+// are, and all groups are of one size.
+template <typename T>
+__device__ __forceinline__ T size_term(T s) {
+  return s == s ? s : (T)0;
+}
+
 // A lane's value in every lane.
 __device__ __forceinline__ float from_lane(float v, int l) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
@@ -190,7 +197,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
       double t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        const double w = key[v] == 0 ? -INFINITY : (a.bias || a.group_top == 1 ? c[v] : s[v]);
+        const double w = key[v] == 0 ? -INFINITY : (a.bias || a.group_top == 1 ? c[v] : size_term(s[v]));
         t2 = fmax(t2, fmin(t1, w));
         t1 = fmax(t1, w);
       }
@@ -218,7 +225,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, int64_t tok, double
       for (int v = 0; v < V; v++) {
         const int e = lane * V + v;
         if (e < g * per || e >= (g + 1) * per) continue;
-        const double w = a.bias ? c[v] : s[v];
+        const double w = a.bias ? c[v] : size_term(s[v]);
         if (key[v] > best) {
           second = best;
           b2 = b1;
@@ -404,7 +411,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
     const bool open = x[v] > -INFINITY && order > -INFINITY;     // neither -inf nor NaN
     key[v] = !open ? 0 : (whole ? (key_of(order) & ~0xFFFFu) | (0xFFFF - e0 - v)
                                 : (key_of(order) & ~15u) | (15 - v));
-    const float w = open ? (by_score ? c[v] : x[v]) : -INFINITY;
+    const float w = open ? (by_score ? size_term(c[v]) : x[v]) : -INFINITY;
     t2 = fmaxf(t2, fminf(t1, w));
     t1 = fmaxf(t1, w);
   }

@@ -456,7 +456,8 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
  * (a quotient in the range of fp32 where the scores leave it; sigmoids of
  * logits that are all below -708 give weights 0).
  * Places without a candidate get expert -1 and weight 0.  A NaN or +inf among
- * softmax's logits makes the weights of its chosen experts NaN. */
+ * softmax's logits makes the weights of its chosen experts NaN; sizes of groups
+ * that would be NaN count as equal. */
 typedef struct {
   const void* logits;          /* fp32 or bf16, aligned to its elements       */
   int64_t stride;              /* elements between tokens, at least experts   */
