@@ -336,7 +336,8 @@ __device__ __forceinline__ uint32_t token_top(uint32_t v) {
 // 2^-22 (sigmoid: exponential, sum, reciprocal) or 2^-19 (softmax: also a sum of up
 // to 22 terms in a run) at most, a sum with a bias by 2^-24 of itself more, and
 // a key drops up to 15 steps of 2^-24.  Two values further apart than `base`
-// (1 + |value|) are in their true order.
+// (1 + |value|) are in their true order.  A group's size of two of them is off by
+// twice as much and 2^-24 of what it sums: by `base_sum` (1 + |terms|) at most.
 __device__ __forceinline__ bool apart(float high, float low, float base) {
   return high - low > base * (1.0f + fabsf(high));
 }
@@ -431,10 +432,14 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
       ahead += o > size || (o == size && g < own);
     }
     const bool stays = t1 > -INFINITY && ahead < a.top_groups;
-    if (by_score) {                      // the smallest that stays and the largest that goes
-      const float low = -token_max<LPT>(stays ? -size : -INFINITY);
-      const float high = token_max<LPT>(stays ? -INFINITY : size);
-      if (low < INFINITY && high > -INFINITY && !apart(low, high, 2.0f * base_sum)) clear = false;
+    if (by_score) {
+      // the smallest that stays and the largest that goes, each by as much as its terms,
+      // which may cancel, can be off; infinite sizes are exact
+      const float terms = fabsf(t1) + (a.group_top == 2 && t2 > -INFINITY ? fabsf(t2) : 0.0f);
+      const float off = fabsf(size) < INFINITY ? base_sum * (1.0f + terms) : 0.0f;
+      const float low = -token_max<LPT>(stays ? off - size : -INFINITY);
+      const float high = token_max<LPT>(stays ? -INFINITY : size + off);
+      if (low < INFINITY && high > -INFINITY && !(low > high)) clear = false;
     }
     if (!stays)
 #pragma unroll

@@ -1,4 +1,5 @@
-"""Routing by groups at the ends of the numbers: tokens whose scores are NaN."""
+"""Routing by groups at the ends of the numbers: tokens whose scores are NaN,
+groups' sizes in which large numbers cancel or stand apart."""
 import math
 
 import pytest
@@ -10,6 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import block_scaled_fp4_reduce_amd as fp4  # noqa: E402
+from test_gpu_route import case, check  # noqa: E402
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -40,3 +42,35 @@ def test_scores_that_are_nan(dtype, renormalize, experts, groups, top_groups, k,
         assert e[t].tolist() == want
         there = e[t] >= 0
         assert w[t][there].isnan().all() and (w[t][~there] == 0).all()
+
+
+def sized(seed, tokens, experts, groups, far):
+    """Logits, and a bias by which a group's two largest sums are far from 0 and cancel."""
+    g = torch.Generator().manual_seed(seed)
+    per = experts // groups
+    bias = torch.full((groups, per), -far)
+    bias[:, 0] = far
+    return torch.randn(tokens, experts, generator=g), bias.flatten()
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", [1.0, 40.0, 3e3, 1e6])
+@pytest.mark.parametrize("experts,groups,top_groups,k", [
+    (64, 8, 4, 4), (64, 8, 4, 6), (60, 5, 2, 2), (256, 8, 3, 3), (256, 8, 3, 15), (128, 8, 2, 20),
+    (320, 64, 5, 5), (512, 32, 7, 7), (512, 32, 7, 9)])
+def test_sizes_that_cancel(scores, far, experts, groups, top_groups, k):
+    logits, bias = sized(experts + k, 40, experts, groups, far)
+    check(case(k, scores, groups, top_groups, 2), logits, bias)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", [1e9, 3e38, math.inf])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_far_away(scores, far, group_top):
+    """Whole groups that a bias puts last or first."""
+    logits, bias = sized(7, 30, 256, 8, 0.25)
+    bias[32:64] = -far
+    bias[96] = far
+    if math.isfinite(far):
+        bias[100] = far
+    check(case(6, scores, 8, 3, group_top), logits, bias)
