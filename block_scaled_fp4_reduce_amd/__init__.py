@@ -418,11 +418,13 @@ def _ints(x, dtype, shape, what):
 
 
 class _Address(int):
-    """The address of a handle's struct, with the device of its buffers."""
+    """The address of a handle's struct, with the device of its buffers and what
+    among them may require a gradient."""
 
-    def __new__(cls, struct, device_index):
+    def __new__(cls, struct, device_index, alpha=None):
         at = super().__new__(cls, C.addressof(struct))
         at.device_index = device_index
+        at.alpha = alpha
         return at
 
 
@@ -641,7 +643,7 @@ class Fp4Weights:
         c = _CWeights(codes.data_ptr(), scales.data_ptr(), _ptr(alpha), experts, rows, cols, fmt,
                       flags)
         for name, value in zip(self.__slots__, (codes, scales, alpha, fmt, flags, experts, rows, cols,
-                                                c, _Address(c, codes.device.index))):
+                                                c, _Address(c, codes.device.index, alpha))):
             object.__setattr__(self, name, value)
 
     def __setattr__(self, name, value):
@@ -657,8 +659,8 @@ class Fp4Weights:
 def fp4_linear(w, x, dtype=None, out=None, ws=None, stream=None):
     """x [tokens][cols] (bf16) times the transpose of FP4 weights ``w``
     [rows][cols]: [tokens][rows] in bf16, or float32 with ``dtype``.  The
-    products are exact and summed in fp32.  There is no backward: an x that
-    requires a gradient is refused in grad mode."""
+    products are exact and summed in fp32.  There is no backward: an x or an
+    alpha that requires a gradient is refused in grad mode."""
     torch = _torch()
     if dtype not in (None, torch.bfloat16, torch.float32):
         raise TypeError("dtype must be bfloat16 or float32, got %s" % (dtype,))

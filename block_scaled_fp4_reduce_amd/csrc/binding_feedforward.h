@@ -66,8 +66,16 @@ void same_device(PyObject* handle, const at::Tensor& x) {
                                ") than the tensors: " + x.device().str());
 }
 
-void no_backward(const char* name, PyObject* const* a, int n) {
-  if (wants_gradient(a, n))
+// Neither a tensor nor the alpha of the handle's weights wants a gradient.
+void no_backward(const char* name, PyObject* handle, PyObject* const* a, int n) {
+  bool wanted = wants_gradient(a, n);
+  if (!wanted && !PyLong_CheckExact(handle)) {
+    PyObject* alpha = PyObject_GetAttrString(handle, "alpha");
+    if (!alpha) throw PyError{};
+    wanted = wants_gradient(&alpha, 1);
+    Py_DECREF(alpha);
+  }
+  if (wanted)
     fail(PyExc_RuntimeError, std::string(name) + " has no backward, but a tensor requires a gradient: "
                              "detach it or call under torch.no_grad()");
 }
@@ -75,7 +83,7 @@ void no_backward(const char* name, PyObject* const* a, int n) {
 // linear(weights, x, dtype is float32, out, ws, stream) -> out
 PyObject* linear(PyObject* const* a) {
   PyObject* const floats[] = {a[1], a[3]};
-  no_backward("fp4_linear", floats, 2);
+  no_backward("fp4_linear", a[0], floats, 2);
   const fp4_weights* w = weights_of(a[0]);
   PyObject* const all[] = {a[1], a[3], a[4]};
   one_device(all, 3);
@@ -98,7 +106,8 @@ PyObject* linear(PyObject* const* a) {
 // experts(gate_up, down, x, weights, experts, out, ws, stream) -> out
 PyObject* experts(PyObject* const* a) {
   PyObject* const floats[] = {a[2], a[3], a[5]};
-  no_backward("fp4_experts", floats, 3);
+  no_backward("fp4_experts", a[0], floats, 3);
+  no_backward("fp4_experts", a[1], nullptr, 0);
   const fp4_weights *gu = weights_of(a[0]), *dn = weights_of(a[1]);
   PyObject* const all[] = {a[2], a[3], a[4], a[5], a[6]};
   one_device(all, 5);
