@@ -15,6 +15,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPGuard.h>
@@ -145,12 +146,28 @@ void check(const char* fn, int status) {
   throw PyError{};
 }
 
-// Whether one of the tensors among a[0 .. n - 1] requires a gradient, in grad mode.
-bool wants_gradient(PyObject* const* a, int n) {
-  if (!at::GradMode::is_enabled()) return false;
+// Whether one of the tensors among a[0 .. n - 1] has a tangent of forward-mode
+// differentiation (which torch.no_grad leaves on).
+bool has_tangent(PyObject* const* a, int n) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return false;
   for (int i = 0; i < n; i++)
-    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i])._fw_grad(0).defined()) return true;
   return false;
+}
+
+// Whether one of them requires a gradient, in grad mode, or has a tangent.
+bool wants_gradient(PyObject* const* a, int n) {
+  if (at::GradMode::is_enabled())
+    for (int i = 0; i < n; i++)
+      if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+  return has_tangent(a, n);
+}
+
+// The calls of gradients have no derivative of their own.
+void no_tangent(const char* name, PyObject* const* a, int n) {
+  if (has_tangent(a, n))
+    fail(PyExc_RuntimeError, std::string(name) + " has no derivative, but a tensor carries a "
+                             "forward-mode gradient");
 }
 
 // The caller's tensor, which counts as modified from here on, or a new one.
@@ -393,6 +410,7 @@ PyObject* norm_rope_backward(PyObject* const* a) {
   PyObject* given[2];
   pair_of(a[10], &given[0], &given[1]);
   PyObject* const all[] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[11], given[0], given[1]};
+  no_tangent("qk_norm_rope_backward", all, 11);
   one_device(all, 11);
   const fp4_qk_rope x = rope_of(a + 2);
   const at::Tensor &q = tensor(a[2], "q"), &k = tensor(a[3], "k");

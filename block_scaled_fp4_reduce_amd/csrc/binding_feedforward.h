@@ -199,6 +199,7 @@ PyObject* route(PyObject* const* a) {
 // route_backward(dweights, logits, experts, scores, renormalize, scale, out, stream) -> dlogits
 PyObject* route_backward(PyObject* const* a) {
   PyObject* const all[] = {a[0], a[1], a[2], a[6]};
+  no_tangent("expert_route_backward", all, 4);
   one_device(all, 4);
   const at::Tensor &l = tensor(a[1], "logits"), &ids = tensor(a[2], "experts");
   const fp4_routing x = routing_of(a[1], ids.dim() == 2 ? ids.size(1) : 0, a[3], a[4], a[5]);
@@ -274,6 +275,7 @@ PyObject* residual_backward(PyObject* const* a) {
   PyObject* given[2];
   pair_of(a[9], &given[0], &given[1]);
   PyObject* const all[] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], given[0], given[1], a[10]};
+  no_tangent("residual_norm_backward", all, 10);
   one_device(all, 10);
   const fp4_residual r = residual_of(a + 2);
   const at::Tensor& x = tensor(a[2], "x");
