@@ -17,11 +17,15 @@ constexpr int kThreads = 256;             // 4 wave64s per workgroup
 
 // Host: launch `kernel` on `st` and return that launch's own status
 // (hipLaunchKernel's return value), so a failure left behind by an earlier,
-// unrelated HIP call of the caller is neither reported nor consumed.
+// unrelated HIP call of the caller is neither reported nor consumed.  A launch of
+// 2^32 threads or more would report success and run with their number cut to 32
+// bits: it is an error here.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
 template <typename... P, typename... A>
 inline hipError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, hipStream_t st,
                          A... a) {
   static_assert(sizeof...(P) == sizeof...(A), "argument count");
+  if ((int64_t)grid * block > kMaxThreads) return hipErrorInvalidConfiguration;
   std::tuple<P...> args{static_cast<P>(a)...};
   return std::apply(
       [&](auto&... v) {

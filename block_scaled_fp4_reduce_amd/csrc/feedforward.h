@@ -62,6 +62,24 @@ inline int check_rows(int64_t tokens, int64_t stride, int64_t width, int64_t mul
   return tokens > 0 && stride > kMaxElems / tokens ? FP4_E_SHAPE : FP4_OK;
 }
 
+// f(first, count) for slices of the tokens, one after another, each of as many as a
+// launch of workgroups of `threads` threads and `per_group` tokens can have.
+template <typename F>
+hipError_t in_slices(int64_t tokens, int64_t per_group, int64_t threads, F&& f) {
+  const int64_t most = kMaxThreads / threads * per_group;
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < tokens && err == hipSuccess; t += most)
+    err = f(t, tokens - t < most ? tokens - t : most);
+  return err;
+}
+
+// Tokens of a slice of a product with `rows` rows: the forms' launches stay within
+// kMaxThreads (32 threads a token and 128 rows at most, with as many left over).
+inline int64_t linear_slice(int64_t rows) {
+  const int64_t most = ((int64_t)1 << 33) / rows & ~(int64_t)127;
+  return most < (1 << 24) ? most : 1 << 24;
+}
+
 // ------------------------------------------------------------------ few tokens
 // Waves that share a row's K, the fewest that give every CU two workgroups (or
 // have a step of K each): fewer meet in fewer joins.
@@ -193,6 +211,40 @@ inline bool tiles_sooner(int64_t tokens, int64_t rows) {
   const int64_t tiles = cdiv(tokens, kTileTokens) * cdiv(rows, kTileWeights);
   const int64_t mids = cdiv(tokens, 64) * cdiv(rows, 64);
   return tokens > 64 && 13 * cdiv(tiles, num_cus()) <= 2 * cdiv(mids, num_cus());
+}
+
+// A slice of a product's tokens.
+inline hipError_t linear_call(const fp4_weights* w, const uint16_t* x, int64_t x_stride,
+                              int64_t tokens, void* out, int64_t out_stride, bool out_f32,
+                              hipStream_t st) {
+  ColsArgs a = {};
+  a.w = weight_view(w);
+  a.x = x;
+  a.out = out;
+  a.xs = x_stride;
+  a.os = out_stride;
+  a.tokens = tokens;
+  a.out_f32 = out_f32;
+  a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
+  if (w->cols > 0 && tiles_sooner(tokens, w->rows)) {
+    TiledArgs t = tiled_args(a);
+    t.tiles_t = (uint32_t)cdiv(tokens, kTileTokens);
+    t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
+    return launch_tiled<false, false>(w->format, t, st);
+  }
+  if (tokens <= 16 && streams_sooner(w, tokens))
+    return launch_stream<false, kDense>(w->format, a, 1, 1, tokens, st);
+  if (tokens <= 16 || w->cols < kMidLeast) {
+    const int64_t slots = cdiv(tokens, 16);
+    return tall(w->rows, slots) ? launch_cols<2, false, kDense>(w->format, a, slots, st)
+                                : launch_cols<1, false, kDense>(w->format, a, slots, st);
+  }
+  switch (linear_tiles(tokens, w->rows)) {
+    case 1: return launch_mid<1>(w->format, a, st);
+    case 2: return launch_mid<2>(w->format, a, st);
+    case 3: return launch_mid<3>(w->format, a, st);
+    default: return launch_mid<4>(w->format, a, st);
+  }
 }
 
 // ------------------------------------------------------------------ experts
@@ -368,6 +420,13 @@ inline RouteArgs route_args(const fp4_routing* r) {
   return a;
 }
 
+// n tokens from the t-th on.
+inline RouteArgs route_slice(RouteArgs a, const fp4_routing* r, int64_t t, int64_t n) {
+  a.logits = (const uint8_t*)a.logits + t * a.stride * (r->logits_bf16 ? 2 : 4);
+  a.tokens = n;
+  return a;
+}
+
 // Sixteen lanes a token where they hold its experts, 16 each, and its choices and
 // one more.
 inline bool route_narrow(const RouteArgs& a) { return a.experts <= 256 && a.top_k <= 15; }
@@ -478,35 +537,13 @@ int fp4_linear(const fp4_weights* w, const uint16_t* x, int64_t x_stride, int64_
   if (x_stride >= kMaxXStride) return FP4_E_SHAPE;
   if (int rc = check_rows(tokens, out_stride, w->rows, 1)) return rc;
   if (!aligned(x, 16) || !aligned(out, out_f32 ? 4 : 2)) return FP4_E_ALIGN;
-  ColsArgs a = {};
-  a.w = weight_view(w);
-  a.x = x;
-  a.out = out;
-  a.xs = x_stride;
-  a.os = out_stride;
-  a.tokens = tokens;
-  a.out_f32 = out_f32 != 0;
-  a.out_vec = out_stride % 4 == 0 && aligned(out, out_f32 ? 16 : 8);
-  hipStream_t st = (hipStream_t)stream;
-  if (w->cols > 0 && tiles_sooner(tokens, w->rows)) {
-    TiledArgs t = tiled_args(a);
-    t.tiles_t = (uint32_t)cdiv(tokens, kTileTokens);
-    t.out_vec = out_stride % (out_f32 ? 4 : 8) == 0 && aligned(out, 16);
-    return launched(launch_tiled<false, false>(w->format, t, st));
-  }
-  if (tokens <= 16 && streams_sooner(w, tokens))
-    return launched(launch_stream<false, kDense>(w->format, a, 1, 1, tokens, st));
-  if (tokens <= 16 || w->cols < kMidLeast) {
-    const int64_t slots = cdiv(tokens, 16);
-    return launched(tall(w->rows, slots) ? launch_cols<2, false, kDense>(w->format, a, slots, st)
-                                         : launch_cols<1, false, kDense>(w->format, a, slots, st));
-  }
-  switch (linear_tiles(tokens, w->rows)) {
-    case 1: return launched(launch_mid<1>(w->format, a, st));
-    case 2: return launched(launch_mid<2>(w->format, a, st));
-    case 3: return launched(launch_mid<3>(w->format, a, st));
-    default: return launched(launch_mid<4>(w->format, a, st));
-  }
+  const int64_t most = linear_slice(w->rows);
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < tokens && err == hipSuccess; t += most)
+    err = linear_call(w, x + t * x_stride, x_stride, tokens - t < most ? tokens - t : most,
+                      (uint8_t*)out + t * out_stride * (out_f32 ? 4 : 2), out_stride, out_f32 != 0,
+                      (hipStream_t)stream);
+  return launched(err);
 }
 
 int expert_route(const fp4_routing* r, float* weights, int32_t* experts, void* stream) {
@@ -521,8 +558,11 @@ int expert_route(const fp4_routing* r, float* weights, int32_t* experts, void* s
   return launched(route_variant(a, [&](auto lpt, auto v) {
     constexpr int L = decltype(lpt)::value, V = decltype(v)::value, V64 = (L * V + 63) / 64;
     auto go = [&](auto kernel, int tokens) {
-      return launch(kernel, (unsigned)cdiv(a.tokens, kRouteWaves * tokens), kRouteThreads,
-                    (hipStream_t)stream, a, weights, experts);
+      return in_slices(r->tokens, kRouteWaves * tokens, kRouteThreads, [&](int64_t t, int64_t n) {
+        return launch(kernel, (unsigned)cdiv(n, kRouteWaves * tokens), kRouteThreads,
+                      (hipStream_t)stream, route_slice(a, r, t, n), weights + t * a.top_k,
+                      experts + t * a.top_k);
+      });
     };
     if (!route_lanes(a, L, V) || a.top_k >= L)
       return r->logits_bf16 ? go(expert_route64_kernel<V64, true>, 1)
@@ -547,8 +587,13 @@ int expert_route_backward(const fp4_routing* r, const float* dweights, const int
   return launched(route_variant(a, [&](auto lpt, auto v) {
     constexpr int L = decltype(lpt)::value, V = decltype(v)::value;
     auto go = [&](auto kernel) {
-      return launch(kernel, (unsigned)cdiv(a.tokens, kRouteWaves * (64 / L)), kRouteThreads,
-                    (hipStream_t)stream, a, dweights, experts, dlogits, dlogits_stride);
+      constexpr int G = kRouteWaves * (64 / L);
+      return in_slices(r->tokens, G, kRouteThreads, [&](int64_t t, int64_t n) {
+        return launch(kernel, (unsigned)cdiv(n, G), kRouteThreads, (hipStream_t)stream,
+                      route_slice(a, r, t, n), dweights + t * a.top_k, experts + t * a.top_k,
+                      (uint8_t*)dlogits + t * dlogits_stride * (r->logits_bf16 ? 2 : 4),
+                      dlogits_stride);
+      });
     };
     return r->logits_bf16 ? go(expert_route_backward_kernel<L, V, true>)
                           : go(expert_route_backward_kernel<L, V, false>);
@@ -602,8 +647,16 @@ int residual_norm(const fp4_residual* a, uint16_t* y, int64_t y_stride, uint16_t
   const ResidualArgs r = residual_args(a);
   return launched(residual_variant(a->dim, [&](auto wpr, auto ch) {
     constexpr int W = decltype(wpr)::value, CH = decltype(ch)::value;
-    return launch(residual_norm_kernel<W, CH>, (unsigned)cdiv(r.tokens, RowShape<W>::kRows),
-                  RowShape<W>::kAll, (hipStream_t)stream, r, y, y_stride, z, z_stride);
+    using S = RowShape<W>;
+    return in_slices(r.tokens, S::kRows, S::kAll, [&](int64_t t, int64_t n) {
+      ResidualArgs part = r;
+      part.x += t * r.xs;
+      part.b += t * r.bs;
+      if (r.gate && r.token_gate) part.gate += t;
+      part.tokens = n;
+      return launch(residual_norm_kernel<W, CH>, (unsigned)cdiv(n, S::kRows), S::kAll,
+                    (hipStream_t)stream, part, y + t * y_stride, y_stride, z + t * z_stride, z_stride);
+    });
   }));
 }
 
