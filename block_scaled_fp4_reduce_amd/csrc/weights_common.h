@@ -92,8 +92,13 @@ __device__ __forceinline__ void wait_lds() {
   asm volatile("" ::: "memory");
 }
 
-// silu(g) u.  The exponential overflows to infinity below -88: silu is -0 there.
+// silu(g) u.  Where e^-g leaves fp32 (g below -88.7) silu is g e^g, whose product
+// with u need not be small: e^(g/2) twice.
 __device__ __forceinline__ float silu_times(float g, float u) {
+  if (g < -88.0f) {
+    const float h = expf(0.5f * g);
+    return g * h * u * h;
+  }
   return g / (1.0f + expf(-g)) * u;
 }
 
