@@ -154,11 +154,14 @@ template <bool GATED>
 __device__ __forceinline__ void put_rows(const ColsArgs& a, int64_t e, int rows, int n, int64_t orow,
                                          float all, const f32x4_t (&v)[GATED ? 2 : 1]) {
   float y[4];
+  auto sum = [&](int h, int i) {         // of projection h
+    return v[h][i] * alpha_row(a.w, e, (n + i < rows ? n + i : rows - 1) + h * rows, all);
+  };
+  if constexpr (GATED) {
+    silu_times(y, [&](int i) { return sum(0, i); }, [&](int i) { return sum(1, i); });
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int row = n + i < rows ? n + i : rows - 1;
-    y[i] = v[0][i] * alpha_row(a.w, e, row, all);
-    if constexpr (GATED) y[i] = silu_times(y[i], v[1][i] * alpha_row(a.w, e, row + rows, all));
+    for (int i = 0; i < 4; i++) y[i] = sum(0, i);
   }
   const int64_t o = orow * a.os + n;
   if (a.out_f32) {

@@ -260,11 +260,15 @@ __global__ __launch_bounds__(kTiledThreads, 2) void fp4_tiled_kernel(TiledArgs a
     for (int i = 0; i < (GATED ? 1 : 2); i++) {
       const int nb = n0 + 32 * i;
       float y[16];
-#pragma unroll
-      for (int v = 0; v < 16; v++) {
+      auto sum = [&](int h, int v) {     // of row tile i, or of projection h
         const int n = nb + 8 * (v / 4) + 4 * hh + v % 4, row = n < rows ? n : rows - 1;
-        y[v] = acc[i][j][v] * alpha_row(a.w, e, row, all);
-        if constexpr (GATED) y[v] = silu_times(y[v], acc[1][j][v] * alpha_row(a.w, e, row + rows, all));
+        return acc[GATED ? h : i][j][v] * alpha_row(a.w, e, row + h * rows, all);
+      };
+      if constexpr (GATED) {
+        silu_times(y, [&](int v) { return sum(0, v); }, [&](int v) { return sum(1, v); });
+      } else {
+#pragma unroll
+        for (int v = 0; v < 16; v++) y[v] = sum(0, v);
       }
       if (a.out_f32) {
         if (c >= count) continue;
