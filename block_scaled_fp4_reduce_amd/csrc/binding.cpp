@@ -1,8 +1,8 @@
 // binding.cpp -- the Python calls of the FP4 cache, its attention, the norm with
-// rotation and the feed-forward operators (binding_feedforward.h): checks of the tensors, allocation of outputs and workspace,
-// and the call into libfp4q.so.  These calls are short (a decoding step's
-// kernels take microseconds), so their checks run here rather than in Python:
-// the norm of one decoding batch takes 5.5 us a call (17.3 through ctypes and torch.empty).
+// rotation and the feed-forward operators (binding_feedforward.h): checks of the
+// tensors, allocation of outputs and workspace, and the call into libfp4q.so.
+// These calls are short (a decoding step's kernels take microseconds), so their
+// checks run here rather than in Python: the norm of one decoding batch takes 5.5 us a call (17.3 through ctypes and torch.empty).
 //
 // Errors: TypeError for a wrong dtype, ValueError for a wrong shape, layout or
 // device, Fp4Error for a status of the library, RuntimeError where a gradient

@@ -204,9 +204,10 @@ inline bool tall(int64_t rows, int64_t slots) {
   return cdiv(rows, 32) * slots * 4 >= 3 * (int64_t)num_cus();
 }
 
-// A round of 128x256 tiles takes as long as six and a half of 64 tokens x 64 rows
-// (88 us and 14 with 4096 columns, whose tiles decode their weights for twice
-// the tokens but wait for each other): whichever has done sooner.
+// A round of 128x256 tiles, one a CU, takes as long as six and a half of 64 tokens
+// x 64 rows (88 us and 14 with 4096 columns): whichever has done sooner.  Of several
+// rounds two tiles share a CU and take less than twice as long (256 tiles 94 us, 512
+// 139, 1024 290), far beyond the sizes at which the two forms meet.
 inline bool tiles_sooner(int64_t tokens, int64_t rows) {
   const int64_t tiles = cdiv(tokens, kTileTokens) * cdiv(rows, kTileWeights);
   const int64_t mids = cdiv(tokens, 64) * cdiv(rows, 64);

@@ -337,9 +337,10 @@ struct ChunkScales {
 // chunks among them.  Eight waves: one alone on its SIMD issues half of what two
 // do.  Two more only fetch the activations: loads come back in a wave's order,
 // and one that waited for activations would wait for all codes that it asked for
-// before, from farther away.  Decoding and its waits bound it: 48 tokens through
-// 14336x4096 of MXFP4 15.0 us (codes, activations and outputs at the rate of a
-// copy: 6.7), by fp4_cols_kernel 23.
+// before, from farther away.  48 tokens through 14336x4096 of MXFP4 take 15.0 us
+// (codes, activations and outputs at the rate of a copy: 6.7), by fp4_cols_kernel 23.
+// No unit is at its limit (vector 35% of the time, matrix 19%): waves wait for their
+// loads, of which a CU has 32 KB of codes under way.
 constexpr int kMidWaves = 8, kMidLoaders = 2, kMidThreads = (kMidWaves + kMidLoaders) * 64;
 constexpr int kMidDepth = 2, kMidChunk = 128;
 constexpr int kMidLeast = 128;           // cols: a dword of scales in every row

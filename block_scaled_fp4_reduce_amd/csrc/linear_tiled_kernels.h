@@ -16,11 +16,14 @@
 // workgroup meets, and the loads of the stage after that go out: they have a
 // whole stage to arrive.
 //
-// 8192 tokens through 14336x4096 (NVFP4): 850 us, 1.13 PFLOP/s; a library's product
-// of the same size with weights in bf16 716.  Left are the waits at a stage's
-// barrier and the decode's issue, with one wave a SIMD: the sums alone take 128 of
-// its registers.  Experts' tiles are short (4096 tokens, 6 of 64 experts, 2048 x
-// 1408: 585 and 540 TFLOP/s), so their first loads and last stores weigh more.
+// 8192 tokens through 14336x4096: NVFP4 831 to 950 us as the clock allows (1.16
+// PFLOP/s), MXFP4 853; a library's product of the same size with weights in bf16
+// 716.  Two workgroups share a CU, so two waves a SIMD, of 256 registers each: the
+// sums take 128, and all but one form keep 2 to 12 values in scratch.  The matrix
+// unit is busy 58% of the time and the vector unit, with the decode, 47%; waves wait
+// 39%, at a stage's barrier and for its loads.  Experts' tiles are short (4096
+// tokens, 6 of 64 experts, 2048 x 1408, NVFP4: gate and up 411 us, down 257, 600 and
+// 480 TFLOP/s), so their first loads and last stores weigh more.
 //
 // LDS layout of a stage: 256 bytes a token, its 16-byte chunk c at position
 // c ^ (token % 16), so that the reads of 16 tokens cover all banks.

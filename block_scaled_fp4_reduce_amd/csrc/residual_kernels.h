@@ -11,12 +11,14 @@
 //
 // A row belongs to 1, 4 or 16 waves, a thread holds 8 consecutive values
 // (one 16-byte load) of each of its CH chunks, and everything stays in registers
-// between the one read and the one write.  The backward pass reads x again and
-// makes y from it: the same bytes as reading y, which is rounded.  All fp32
-// but for the squares' sums that leave its range (Rms below) and the
-// tokens' sums, which are joined in 64 bits.  Memory bounds it: 8192 tokens of 4096
-// channels 50 us forward (5.4 TB/s), 95 backward (4.2 TB/s) and 7 for the weights'
-// sums.
+// between the one read and the one write, but for the backward pass of more than
+// 8192 channels: a thread of 16 waves has 128 registers, and 641 values go to
+// scratch (4096 tokens of 16384 channels 4.85 ms; of 8192 channels 0.12).  The
+// backward pass reads x again and makes y from it: the same bytes as reading y,
+// which is rounded.  All fp32 but for the squares' sums that leave its range (Rms
+// below) and the tokens' sums, which are joined in 64 bits.  Memory bounds the rest:
+// 8192 tokens of 4096 channels 50 us forward (5.4 TB/s), 95 backward (4.2 TB/s) and
+// 7 for the weights' sums; forward 4096 tokens of 16384 channels 114 (4.7 TB/s).
 #pragma once
 
 #include "kv_common.h"

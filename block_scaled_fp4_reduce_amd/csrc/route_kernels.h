@@ -9,11 +9,11 @@
 //     sigmoid, renormalized  dl_i = scale p_i (1 - s_i) (g_i - sum_j p_j g_j)
 //     sigmoid                dl_i = scale s_i (1 - s_i) g_i
 //
-// Instructions bound it, so a token belongs to 16 lanes (64 past 256 experts or
-// 16 choices): 4 tokens share each one.  A lane holds up to 16 consecutive
-// experts as 32-bit keys in the order of c, the number within the lane in the
-// lowest 4 bits, so that a maximum is one instruction and names its expert.  The
-// first top_k + 1 of them are put in order by their exact logits or sums in 64
+// Instructions bound the forward, so a token belongs to 16 lanes (64 past 256
+// experts or 15 choices): 4 tokens share each one.  A lane holds up to 16
+// consecutive experts as 32-bit keys in the order of c, the number within the lane
+// in the lowest 4 bits, so that a maximum is one instruction and names its expert.
+// The first top_k + 1 of them are put in order by their exact logits or sums in 64
 // bits; where one more might belong to them, or the groups' sizes are too close
 // for fp32 (about one token in 10^4), the wave does the token again in 64 bits.
 //
@@ -22,8 +22,9 @@
 // scores themselves may lie below fp32: sigmoids of logits below -88, and with a
 // bias softmax's of logits that far below the largest.
 //
-// 16384 tokens of 256 experts, sigmoid, bias, 4 of 8 groups, 8 chosen: 17.0 us
-// forward and 11.5 backward; forward by a wave a token 28.7, all in 64 bits 48.8.
+// 16384 tokens of 256 experts, sigmoid, bias, 4 of 8 groups, 8 chosen: 17.7 us
+// forward (the vector unit is busy for 75% of it) and 11.6 backward (44%: a lane's
+// stores are a line apart); forward by a wave a token 28.7, all in 64 bits 48.8.
 #pragma once
 
 #include "kv_common.h"

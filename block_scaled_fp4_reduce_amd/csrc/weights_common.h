@@ -28,7 +28,9 @@ struct WeightView {
   int row_alpha;                         // floats from one row's alpha to the next (0 or 1)
 };
 
-// An offset past every buffer here (they end below it): reads as zeros.
+// An offset past every buffer of activations, which the host keeps below it: reads
+// as zeros.  Codes or scales of more bytes than that are read there instead, with
+// activations that are zeros.
 constexpr uint32_t kBufferEnd = 0x7FFFFF00u;
 
 // FMT: FP4_FORMAT_NVFP4 (0) or FP4_FORMAT_MXFP4 (1).

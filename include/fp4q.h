@@ -38,7 +38,8 @@
  *    FP4_E_HIP reports a failed kernel launch (the launch's own return
  *    status; an error left by an earlier, unrelated HIP call is neither
  *    reported nor cleared); faults during execution surface at the caller's
- *    next synchronisation.
+ *    next synchronisation.  A launch of 2^32 threads or more, which HIP would
+ *    cut short without an error, is one that fails.
  *  - Tensors holding Inf/NaN, or (NVFP4) whose largest magnitude is below
  *    2^-64 without being zero, are outside the method's domain: the call
  *    succeeds and never faults, but codes and scales are unspecified.
