@@ -147,11 +147,15 @@ void check(const char* fn, int status) {
 }
 
 // Whether one of the tensors among a[0 .. n - 1] has a tangent of forward-mode
-// differentiation (which torch.no_grad leaves on).
+// differentiation (which torch.no_grad leaves on).  Most tensors have no state of
+// autograd at all, which is seen without a call (0.1 us of a norm's 5).
 bool has_tangent(PyObject* const* a, int n) {
-  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return false;
-  for (int i = 0; i < n; i++)
-    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i])._fw_grad(0).defined()) return true;
+  for (int i = 0; i < n; i++) {
+    if (!THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (t.unsafeGetTensorImpl()->autograd_meta() && t._fw_grad(0).defined())
+      return c10::AutogradState::get_tls_state().get_fw_grad_mode();
+  }
   return false;
 }
 

@@ -490,7 +490,9 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   const bool in = chosen >= 0 && place < a.top_k;
   float s = 0.0f;
   if (a.renormalize) {
-    const float m = token_max<LPT>(in ? choice_top(l, a.sigmoid) : -INFINITY);
+    // softmax's largest logit is chosen itself but for a bias or groups
+    const float m = a.sigmoid || a.bias || a.groups > 1
+                        ? token_max<LPT>(in ? choice_top(l, a.sigmoid) : -INFINITY) : top;
     if (in) s = choice_score(l, m, a.sigmoid);
   } else if (in) {
     s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / total;
